@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_round.so")
-SOURCES = (["moe_round.hip", "moe_validate.cpp"] + [f"moe_gemv_g{g}.hip" for g in (4, 8, 16, 32, 64)]
+SOURCES = (["moe_round.hip", "moe_validate.cpp", "verify_ops.hip", "verify_attention_bf16.hip",
+            "verify_attention_f16.hip", "verify_validate.cpp"] + [f"moe_gemv_g{g}.hip" for g in (4, 8, 16, 32, 64)]
            + [f"moe_gemv_g{g}_s256.hip" for g in (4, 8, 16, 32, 64)])
 
 ARCH = "gfx950"
@@ -32,7 +33,10 @@ FLAGS = [
 # registers) that costs no register-to-register copies. Its other matrix-core kernel (the fp64
 # router GEMM) only stores its results.
 SOURCE_FLAGS = {"moe_round.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "moe_gemv_g16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}  # the down tile's results fold on VALU
+                "moe_gemv_g16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],  # the down tile's results fold on VALU
+                # the scores are masked and exponentiated, the outputs rescaled, on the vector ALUs
+                "verify_attention_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "verify_attention_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

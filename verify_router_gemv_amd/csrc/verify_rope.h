@@ -1,0 +1,157 @@
+// RMS norm of each query and key head, the rotary position, and the cache write, in one pass.
+//
+// A head's D values lie in D / 8 lanes, eight each (one 16-byte load of 16-bit values), so the norm is
+// a reduction over 8, 16 or 32 neighbouring lanes and the pair of value i in the half layout, i + R/2, is
+// the same element of a lane R / 16 further: no shared memory but the row's angles.  A block of 256
+// threads takes one row; its first R / 2 threads compute the angles while the heads' loads are under
+// way.  Angle and reduction to a turn are float64 (position * inv_freq * 1/(2 pi), 53 bits: a position of
+// 2^20 keeps its fraction of a turn to 2^-33), the sine and cosine of the remaining turn float32.  One
+// rounding at the end, to the cache's type.
+// Bound: memory from about a thousand rows, launch and two dependent load latencies below.
+#pragma once
+
+#include "verify_common.h"
+
+namespace verify {
+
+constexpr int kRopeThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ f32x8 load8(const T* p);
+template <>
+__device__ __forceinline__ f32x8 load8<float>(const float* p) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+template <>
+__device__ __forceinline__ f32x8 load8<__bf16>(const __bf16* p) {
+  return __builtin_convertvector(*reinterpret_cast<const bf16x8*>(p), f32x8);
+}
+template <>
+__device__ __forceinline__ f32x8 load8<_Float16>(const _Float16* p) {
+  return __builtin_convertvector(*reinterpret_cast<const f16x8*>(p), f32x8);
+}
+__device__ __forceinline__ void store8(__bf16* p, f32x8 v) {
+  *reinterpret_cast<bf16x8*>(p) = __builtin_convertvector(v, bf16x8);
+}
+__device__ __forceinline__ void store8(_Float16* p, f32x8 v) {
+  *reinterpret_cast<f16x8*>(p) = __builtin_convertvector(v, f16x8);
+}
+
+template <typename TI, typename TC, int D>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(verify_rope_args a) {
+  constexpr int L = D / 8;                 // lanes per head
+  constexpr int HB = kRopeThreads / L;     // heads per step of the block
+  __shared__ float2 turn[D / 2];
+  const int t = blockIdx.x, l = threadIdx.x % L;
+  const int items = a.heads + 2 * a.kv_heads;
+  const int slot = a.slots[t];
+  const int page = slot / a.page_size, place = slot - page * a.page_size;
+  if (slot < 0 || page >= a.n_pages) return;  // the whole block
+
+  auto source = [&](int item) -> const TI* {
+    if (item < a.heads) return static_cast<const TI*>(a.q) + t * a.q_row + item * a.q_head;
+    item -= a.heads;
+    if (item < a.kv_heads) return static_cast<const TI*>(a.k) + t * a.k_row + item * a.k_head;
+    return static_cast<const TI*>(a.v) + t * a.v_row + (item - a.kv_heads) * a.v_head;
+  };
+  int item = blockIdx.y * HB + threadIdx.x / L;
+  f32x8 x{};
+  if (item < items) x = load8<TI>(source(item) + 8 * l);
+
+  const int half = a.n_freq;
+  if (static_cast<int>(threadIdx.x) < half) {
+    const double angle = static_cast<double>(a.positions[t]) * static_cast<double>(a.inv_freq[threadIdx.x]);
+    const double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
+    float s, c;
+    sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
+    turn[threadIdx.x] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  for (;;) {
+    const int next = item + gridDim.y * HB;
+    f32x8 xn{};
+    if (next < items) xn = load8<TI>(source(next) + 8 * l);
+    const bool is_q = item < a.heads, is_v = item >= a.heads + a.kv_heads;
+    // Lanes of a head past the last take part in the shuffles (with zeros) and store nothing.
+    const float* w = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+    f32x8 y = x;
+    float ss = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
+#pragma unroll
+    for (int s = 1; s < L; s <<= 1) ss += __shfl_xor(ss, s);
+    if (w) {
+      const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+      y = x * r * load8<float>(w + 8 * l);
+    }
+    f32x8 z = y;
+    if (a.interleaved) {
+      if (8 * l < 2 * half) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 cs = turn[4 * l + j / 2];
+          z[j] = y[j] * cs.x - y[j + 1] * cs.y;
+          z[j + 1] = y[j + 1] * cs.x + y[j] * cs.y;
+        }
+      }
+    } else {
+      const int hop = half / 8;  // lanes to the other half of the pair
+      const bool low = l < hop, in = l < 2 * hop;
+      const int lane = threadIdx.x & 63;
+      const int from = in ? (low ? lane + hop : lane - hop) : lane;
+      f32x8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __shfl(y[j], from);
+      if (in) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 cs = turn[8 * (low ? l : l - hop) + j];
+          z[j] = y[j] * cs.x + (low ? -o[j] : o[j]) * cs.y;
+        }
+      }
+    }
+    if (item < items) {
+      if (is_q) {
+        store8(static_cast<TC*>(a.q_out) + t * a.o_row + item * a.o_head + 8 * l, z);
+      } else if (!is_v) {
+        store8(static_cast<TC*>(a.k_cache) + page * a.kc_page + (item - a.heads) * a.kc_head + place * a.kc_token + 8 * l, z);
+      } else {
+        store8(static_cast<TC*>(a.v_cache) + page * a.vc_page + (item - a.heads - a.kv_heads) * a.vc_head +
+                   place * a.vc_token + 8 * l, x);
+      }
+    }
+    if (next - static_cast<int>(threadIdx.x / L) >= items) break;  // uniform over the block
+    item = next;
+    x = xn;
+  }
+}
+
+// Rows alone fill the chip from 512 on; below, a row's heads are spread over blocks too (each block
+// computes the row's angles again).
+template <typename TI, typename TC, int D>
+hipError_t launch_rope_t(const verify_rope_args& a, hipStream_t stream) {
+  constexpr int HB = kRopeThreads / (D / 8);
+  const int steps = (a.heads + 2 * a.kv_heads + HB - 1) / HB;
+  rope_kernel<TI, TC, D><<<dim3(a.n_rows, a.n_rows < 512 ? steps : 1), kRopeThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <typename TI, typename TC>
+hipError_t launch_rope_d(const verify_rope_args& a, hipStream_t stream) {
+  switch (a.dim) {
+    case 64: return launch_rope_t<TI, TC, 64>(a, stream);
+    case 128: return launch_rope_t<TI, TC, 128>(a, stream);
+    default: return launch_rope_t<TI, TC, 256>(a, stream);
+  }
+}
+
+inline hipError_t launch_rope(const verify_rope_args& a, hipStream_t stream) {
+  if (a.cache_type == VERIFY_BF16)
+    return a.in_type == VERIFY_F32 ? launch_rope_d<float, __bf16>(a, stream) : launch_rope_d<__bf16, __bf16>(a, stream);
+  return a.in_type == VERIFY_F32 ? launch_rope_d<float, _Float16>(a, stream)
+                                 : launch_rope_d<_Float16, _Float16>(a, stream);
+}
+
+}  // namespace verify
