@@ -159,20 +159,6 @@ struct Mfma<_Float16> {
   static constexpr float kLift = 7.0f;
 };
 
-// The word of lane ^ 16 (X = 16) or lane ^ 32 beside the lane's own, in either order.
-template <int X>
-__device__ __forceinline__ float2 across(float v) {
-  const uint32_t w = __builtin_bit_cast(uint32_t, v);
-  uint32_t a, b;  // scalars: a bit cast of a vector's element would read its first element
-  if constexpr (X == 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-    a = r[0], b = r[1];
-  } else {
-    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-    a = r[0], b = r[1];
-  }
-  return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
-}
 // Maximum / sum over the lanes that hold the other tokens of the same query row.
 __device__ __forceinline__ float rows_max(float v) {
   const float2 a = across<16>(v);

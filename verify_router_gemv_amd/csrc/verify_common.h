@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "moe_common.h"
 #include "verify_ops.h"
 
 namespace verify {
@@ -33,6 +34,59 @@ __device__ __forceinline__ int64_t wave_scan64(int64_t v, int lane) {
   }
   return v;
 }
+
+// The word of lane ^ 16 (X = 16) or lane ^ 32 beside the lane's own, in either order.
+template <int X>
+__device__ __forceinline__ float2 across(float v) {
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  uint32_t a, b;  // scalars: a bit cast of a vector's element would read its first element
+  if constexpr (X == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    a = r[0], b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    a = r[0], b = r[1];
+  }
+  return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+// Reductions over the wave on the vector ALUs; every lane gets the result. Maxima skip NaN.
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, moe::dpp_f32<moe::kDppXor1>(v));
+  v = fmaxf(v, moe::dpp_f32<moe::kDppXor2>(v));
+  v = fmaxf(v, moe::dpp_f32<moe::kDppHalfMirror>(v));
+  v = fmaxf(v, moe::dpp_f32<moe::kDppMirror>(v));
+  float2 a = across<16>(v);
+  a = across<32>(fmaxf(a.x, a.y));
+  return fmaxf(a.x, a.y);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += moe::dpp_f32<moe::kDppXor1>(v);
+  v += moe::dpp_f32<moe::kDppXor2>(v);
+  v += moe::dpp_f32<moe::kDppHalfMirror>(v);
+  v += moe::dpp_f32<moe::kDppMirror>(v);
+  float2 a = across<16>(v);
+  a = across<32>(a.x + a.y);
+  return a.x + a.y;
+}
+__device__ __forceinline__ int wave_max(int v) {
+  v = max(v, static_cast<int>(moe::dpp_u32<moe::kDppXor1>(v)));
+  v = max(v, static_cast<int>(moe::dpp_u32<moe::kDppXor2>(v)));
+  v = max(v, static_cast<int>(moe::dpp_u32<moe::kDppHalfMirror>(v)));
+  v = max(v, static_cast<int>(moe::dpp_u32<moe::kDppMirror>(v)));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(static_cast<int>(a[0]), static_cast<int>(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(static_cast<int>(b[0]), static_cast<int>(b[1]));
+}
+__device__ __forceinline__ int wave_min(int v) {
+#pragma unroll
+  for (int s = 32; s >= 1; s >>= 1) v = min(v, __shfl_xor(v, s));
+  return v;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 __device__ __forceinline__ int max0(int v) { return v > 0 ? v : 0; }
 

@@ -7,10 +7,12 @@
 // and looks at a chunk's elements again only when some lane's maximum (known already) beats the K-th;
 // the wave then takes the chunk's best elements out one by one, largest first, so a chunk costs at most K
 // insertions, and a random row about K ln(n / K) in all.
-// Rows are cut over blocks while there are fewer rows than the chip has room for; a second kernel joins
-// the parts. With enough rows, one block takes a whole row and joins its waves itself.
-// Bound: memory from a few rows of 10^5 logits; a 16-bit row is near the vector rate too (about ten
-// operations an element).
+//
+// All rows' chunks of 1024 logits form one sequence that is cut evenly over the waves the chip holds, so
+// every wave reads the same amount whatever the rows and the vocabulary are; a wave that crosses from one
+// row into the next writes a part per row, and a second kernel joins each row's parts (one wave a row).
+// Bound: memory from a few dozen rows of 10^5 logits (a 16-bit row is near the vector rate too, about
+// twelve issue slots an element); below, launch, load and insertion latency.
 #pragma once
 
 #include "verify_common.h"
@@ -19,7 +21,12 @@ namespace verify {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / 64;
+constexpr int kLpChunk = 1024;      // logits per wave step: 16 a lane
+constexpr int kLpEach = kLpChunk / 64;
+// Waves a SIMD holds at the kernel's registers, by the element's size.
+constexpr int lp_waves(int size) { return size == 4 ? 5 : 6; }
 constexpr int kTop = VERIFY_MAX_ALTERNATIVES;
+static_assert(kTop <= 16, "the list lies in one 16-lane row");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLpNegInf = -__builtin_inff();
 
@@ -28,285 +35,348 @@ struct LpStat {
   float m, l, e;  // reference (in powers of two), sums
 };
 
+// The lanes' statistics as one; every lane gets it.
+__device__ __forceinline__ LpStat lp_wave(LpStat s) {
+  const float m = wave_max(s.m);
+  const float ref = m == kLpNegInf ? 0.0f : m;
+  const float d = s.m == kLpNegInf ? 0.0f : s.m - ref;  // a lane that saw nothing: sums 0 (or NaN)
+  const float f = __builtin_amdgcn_exp2f(d);
+  return {m, wave_sum(s.l * f), wave_sum(f == 0 ? 0.0f : f * (s.e + d * s.l))};
+}
+
+// Two lanes' statistics as one.
 __device__ __forceinline__ LpStat lp_join(LpStat a, LpStat b) {
   const float m = fmaxf(a.m, b.m);
   const float ref = m == kLpNegInf ? 0.0f : m;
-  // an empty side (m = -inf, sums 0) has factor 0 and shift 0
   const float da = a.m == kLpNegInf ? 0.0f : a.m - ref, db = b.m == kLpNegInf ? 0.0f : b.m - ref;
   const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
-  LpStat r;
-  r.m = m;
-  // a factor of 0 times a shift of many thousand must not meet an infinite shift: shifts are finite here
-  r.l = a.l * fa + b.l * fb;
-  r.e = (fa == 0 ? 0.0f : fa * (a.e + da * a.l)) + (fb == 0 ? 0.0f : fb * (b.e + db * b.l));
-  return r;
+  return {m, a.l * fa + b.l * fb, (fa == 0 ? 0.0f : fa * (a.e + da * a.l)) + (fb == 0 ? 0.0f : fb * (b.e + db * b.l))};
 }
 
-// The wave's best elements, sorted: lane i < K holds the i-th. `n` of them are there; `cut` is the K-th
-// value once n = K.
+// Logits as signed integers of the same order, equal exactly where the logits are equal (-0 and 0); NaN is
+// below them all.
+constexpr int kLpNone = INT32_MIN;
+__device__ __forceinline__ int lp_key(float x) {
+  const int b = __builtin_bit_cast(int, x + 0.0f);
+  return x == x ? b ^ ((b >> 31) & 0x7fffffff) : kLpNone;
+}
+__device__ __forceinline__ float lp_unkey(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff)); }
+
+// The wave's best elements as keys, sorted: lane i < n holds the i-th; `cut` and `cut_id` are the K-th once
+// n = K.
 struct LpTop {
-  float v;
-  int id;
-  int n;
-  float cut;
+  int k = 0;
+  int id = -1;
+  int n = 0;
+  int cut = kLpNone;
+  int cut_id = -1;
 };
 
-__device__ __forceinline__ void lp_insert(LpTop& top, float v, int id, int K, int lane) {
+// All but the lists are the same in every lane (scalars).
+__device__ __forceinline__ void lp_insert(LpTop& top, int key, int id, int K, int lane) {
   // after everything larger, and after equal ones of lower id
-  const bool before = lane < top.n && (top.v > v || (top.v == v && top.id < id));
+  const bool before = (lane < top.n) & ((top.k > key) | ((top.k == key) & (top.id < id)));
   const int at = __popcll(__ballot(before));
-  const float vu = __shfl_up(top.v, 1);
-  const int iu = __shfl_up(top.id, 1);
-  if (lane > at) top.v = vu, top.id = iu;
-  if (lane == at) top.v = v, top.id = id;
-  if (top.n < K) ++top.n;
-  if (top.n == K) top.cut = __shfl(top.v, K - 1);
+  // every lane's left neighbour within its 16 lanes
+  const int ku = static_cast<int>(moe::dpp_u32<0x111>(static_cast<uint32_t>(top.k)));
+  const int iu = static_cast<int>(moe::dpp_u32<0x111>(static_cast<uint32_t>(top.id)));
+  top.k = lane == at ? key : lane > at ? ku : top.k;
+  top.id = lane == at ? id : lane > at ? iu : top.id;
+  top.n = uniform(top.n < K ? top.n + 1 : K);
+  if (top.n == K) {
+    top.cut = __builtin_amdgcn_readlane(top.k, K - 1);
+    top.cut_id = __builtin_amdgcn_readlane(top.id, K - 1);
+  }
+}
+__device__ __forceinline__ bool lp_good(const LpTop& top, int key, int id, int K) {
+  return top.n < K || key > top.cut || (key == top.cut && id < top.cut_id);
 }
 
-// Takes the elements of x (E per lane, element j of the lane has id ids(j), ascending in j) that are among
-// the best. Every lane calls it; NaN elements are never taken.
-template <int E, typename F>
-__device__ __forceinline__ void lp_take(LpTop& top, const float (&x)[E], int K, int lane, F ids) {
-  uint64_t left = 0;  // elements of this lane not yet taken
-  static_assert(E <= 64, "one bit an element");
-#pragma unroll
-  for (int j = 0; j < E; ++j) left |= (x[j] == x[j] && ids(j) >= 0) ? uint64_t(1) << j : 0;
-  for (;;) {
-    float best = kLpNegInf;
-    int at = -1;
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (((left >> j) & 1) && (at < 0 || x[j] > best)) best = x[j], at = j;
-    float w = best;
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) w = fmaxf(w, __shfl_xor(w, s));
-    int id = INT32_MAX;
-    if (at >= 0 && best == w) {
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (j == at) id = ids(j);
+// The best K of one candidate per lane (key kLpNone: none), as a new list. Equal keys in ascending order of id.
+__device__ __forceinline__ void lp_first(LpTop& top, int key, int id, int K, int lane) {
+  for (int i = 0; i < K; ++i) {
+    const int w = uniform(wave_max(key));
+    if (w == kLpNone) break;
+    const uint64_t who = __ballot(key == w);
+    int from = __ffsll(static_cast<unsigned long long>(who)) - 1;
+    int lo = __builtin_amdgcn_readlane(id, from);
+    if (who & (who - 1)) {  // equal ones
+      lo = uniform(wave_min(key == w ? id : INT32_MAX));
+      from = __ffsll(static_cast<unsigned long long>(__ballot(key == w && id == lo))) - 1;
     }
-    int lo = id;
+    top.k = lane == i ? w : top.k;
+    top.id = lane == i ? lo : top.id;
+    key = lane == from ? kLpNone : key;
+    top.n = i + 1;
+  }
+  if (top.n == K) {
+    top.cut = __builtin_amdgcn_readlane(top.k, K - 1);
+    top.cut_id = __builtin_amdgcn_readlane(top.id, K - 1);
+  }
+}
+
+// Inserts the candidates of the lanes in `who` that are still good enough, one by one.
+__device__ __forceinline__ void lp_each(LpTop& top, uint64_t who, int key, int id, int K, int lane) {
+  while (who) {
+    const int from = __ffsll(static_cast<unsigned long long>(who)) - 1;
+    who &= who - 1;
+    const int ck = __builtin_amdgcn_readlane(key, from), ci = __builtin_amdgcn_readlane(id, from);
+    if (lp_good(top, ck, ci, K)) lp_insert(top, ck, ci, K, lane);
+  }
+}
+
+// Element j of a lane in a chunk.
+template <int VEC>
+__device__ __forceinline__ int lp_place(int j, int lane) {
+  return (j / VEC * 64 + lane) * VEC + j % VEC;
+}
+
+// Takes those of a chunk's elements that are among the best K: x the lanes' elements (NaN: none), best their
+// largest, base the id of the chunk's first. With a list that is not full, or with many lanes that have
+// something to offer, the lanes' best elements go first: the K best of them are a list already, or raise
+// the cut, so that little is left to insert one by one, whatever the order of the row.
+template <int VEC>
+__device__ __forceinline__ void lp_take(LpTop& top, const float (&x)[kLpEach], float best, int K, int lane, int base) {
+  int done = -1;  // the lane's element that has gone first
+  if (top.n < K || __popcll(__ballot(lp_key(best) > top.cut)) > 4 + K) {
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) lo = min(lo, __shfl_xor(lo, s));
-    if (lo == INT32_MAX) return;  // nothing left
-    if (top.n == K) {  // full: it must beat the last (a tie goes to the lower id)
-      const float lv = __shfl(top.v, K - 1);
-      const int li = __shfl(top.id, K - 1);
-      if (!(w > lv || (w == lv && lo < li))) return;
-    }
-    lp_insert(top, w, lo, K, lane);
-    if (id == lo) left &= ~(uint64_t(1) << at);
+    for (int j = kLpEach - 1; j >= 0; --j) done = x[j] == best ? j : done;
+    LpTop mine;
+    lp_first(mine, lp_key(best), base + lp_place<VEC>(done, lane), K, lane);
+    if (top.n == 0) top = mine;
+    else lp_each(top, (uint64_t(1) << mine.n) - 1, mine.k, mine.id, K, lane);
+  }
+#pragma unroll
+  for (int j = 0; j < kLpEach; ++j) {
+    const float least = top.n < K ? kLpNegInf : lp_unkey(top.cut);
+    const bool may = x[j] >= least;
+    if (!__ballot(may)) continue;
+    const int id = base + lp_place<VEC>(j, lane), key = lp_key(x[j]);
+    lp_each(top, __ballot(may && j != done && lp_good(top, key, id, K)), key, id, K, lane);
   }
 }
 
 struct LpPlan {
-  int32_t splits;   // blocks per row
-  float* stat;      // [rows][splits * 4][3]
-  float* tv;        // [rows][splits * 4][top]
-  int32_t* ti;      // the same
+  int32_t chunks;    // per row
+  int64_t per_wave;  // chunks of a wave, of n_rows * chunks
+  int64_t waves;
+  float* stat;       // [waves + rows][3]: the part of wave w in row t lies at w + t
+  int32_t* tk;       // [waves + rows][top] keys
+  int32_t* ti;       // the same of ids
 };
 
+// Chunk 0 of a row starts at the row's last 16-byte boundary at or before its first element, so all loads
+// but the row's edges are whole and aligned.
 template <typename T>
-__device__ __forceinline__ float lp_value(T v) { return static_cast<float>(v); }
-
-template <typename T>
-__device__ __forceinline__ void lp_outputs(const verify_logprobs_args& a, int t, const LpStat& st, const LpTop& top,
-                                           int lane) {
-  // every lane holds the row's statistics, the first `top` lanes the alternatives
-  const float lg = __builtin_amdgcn_logf(st.l);  // log2
-  const bool none = st.m == kLpNegInf && st.l == 0;  // every logit is -inf
-  const float z = kLn2 * (st.m + lg);
-  const T* row = static_cast<const T*>(a.logits) + t * a.row_stride;
-  for (int n = lane; n < a.n_tokens; n += 64) {
-    const int64_t at = static_cast<int64_t>(t) * a.n_tokens + n;
-    const int64_t id = a.tokens_64 ? static_cast<const int64_t*>(a.tokens)[at] : static_cast<const int32_t*>(a.tokens)[at];
-    float lp = kLpNegInf;
-    if (id >= 0 && id < a.vocab) {
-      const float x = lp_value(row[id]);
-      lp = none ? kLpNegInf : x - z;
-    }
-    a.logprobs[at] = lp;
-  }
-  if (a.entropy && lane == 0) a.entropy[t] = none ? 0.0f : kLn2 * (lg - st.e / st.l);
-  if (lane < a.top) {
-    const int64_t at = static_cast<int64_t>(t) * a.top + lane;
-    const bool there = lane < top.n;
-    a.top_ids[at] = there ? top.id : -1;
-    a.top_logprobs[at] = !there ? __builtin_nanf("") : none ? kLpNegInf : top.v - z;
-  }
-}
-
-// Joins `parts` partial results (statistics and sorted lists of K), one wave.
-template <typename FS, typename FV, typename FI>
-__device__ __forceinline__ void lp_join_parts(int parts, int K, int lane, FS stat, FV value, FI ident, LpStat* st,
-                                              LpTop* top) {
-  LpStat s{kLpNegInf, 0, 0};
-  for (int i = lane; i < parts; i += 64) s = lp_join(s, stat(i));
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const LpStat o{__shfl_xor(s.m, d), __shfl_xor(s.l, d), __shfl_xor(s.e, d)};
-    // the lower lane's side first on both sides, so that all lanes agree bit for bit
-    s = (lane & d) ? lp_join(o, s) : lp_join(s, o);
-  }
-  *st = s;
-  *top = LpTop{0, -1, 0, 0};
-  for (int i0 = 0; i0 < parts * K; i0 += 64) {
-    const int i = i0 + lane;
-    float x[1] = {0};
-    int id = -1;
-    if (i < parts * K) x[0] = value(i), id = ident(i);
-    lp_take<1>(*top, x, K, lane, [&](int) { return id; });
-  }
+__device__ __forceinline__ int lp_offset(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(verify_logprobs_args a, LpPlan p) {
-  constexpr int VEC = 16 / sizeof(T);  // elements of a load
-  constexpr int U = sizeof(T) == 4 ? 4 : 2;
-  constexpr int E = VEC * U, CHUNK = 64 * E;
+__global__ void __launch_bounds__(kLpThreads, lp_waves(sizeof(T))) logprobs_kernel(verify_logprobs_args a, LpPlan p) {
+  constexpr int VEC = 16 / sizeof(T), U = kLpEach / VEC;  // logits of a load, loads of a chunk
   typedef T TV __attribute__((ext_vector_type(VEC)));
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int t = blockIdx.x / p.splits, split = blockIdx.x - t * p.splits;
-  const T* const row = static_cast<const T*>(a.logits) + t * a.row_stride;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kLpWaves + wave;
+  const int64_t all = static_cast<int64_t>(a.n_rows) * p.chunks;
+  const int64_t g0 = w * p.per_wave;
+  const int64_t g1 = g0 + p.per_wave < all ? g0 + p.per_wave : all;
+  if (g0 >= g1) return;
   const int V = a.vocab, K = a.top;
 
-  // The row from its first 16-byte boundary on is cut into chunks, the chunks evenly over the row's waves;
-  // the elements before it go to the first wave, those behind the last whole chunk to the last.
-  const int miss = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / static_cast<int>(sizeof(T));
-  const int lead = miss < V ? miss : V;
-  const int chunks = (V - lead) / CHUNK;
-  const int waves = p.splits * kLpWaves, w = split * kLpWaves + wave;
-  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * w / waves);
-  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (w + 1) / waves);
+  TV buf[U];
+  auto load = [&](int t, int c) {
+    const T* const row = static_cast<const T*>(a.logits) + t * a.row_stride;
+    const int first = c * kLpChunk - lp_offset(row);
+    if (first >= 0 && first + kLpChunk <= V) {
+      const T* const src = row + first;
+#pragma unroll
+      for (int u = 0; u < U; ++u) buf[u] = *reinterpret_cast<const TV*>(src + (u * 64 + lane) * VEC);
+    } else {  // an edge of the row: element by element, from inside it
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const int i = first + (u * 64 + lane) * VEC + j;
+          const T v = row[i < 0 ? 0 : i < V ? i : V - 1];
+          buf[u][j] = i >= 0 && i < V ? v : static_cast<T>(kLpNegInf);
+        }
+    }
+  };
 
   LpStat st{kLpNegInf, 0, 0};
-  LpTop top{0, -1, 0, 0};
-  auto add = [&](const float (&x)[E], auto ids) {
-    float best = kLpNegInf;
+  LpTop top;
+  int t = static_cast<int>(g0 / p.chunks), c = static_cast<int>(g0 - static_cast<int64_t>(t) * p.chunks);
+  load(t, c);
+  for (int left = static_cast<int>(g1 - g0); left > 0; --left) {
+    float x[kLpEach];
 #pragma unroll
-    for (int j = 0; j < E; ++j) best = fmaxf(best, x[j]);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[u * VEC + j] = static_cast<float>(static_cast<T>(buf[u][j]));
+    const int t0 = t, c0 = c;
+    const bool row_ends = c + 1 == p.chunks;
+    if (row_ends) c = 0, ++t;
+    else ++c;
+    if (left > 1) load(t, c);  // the next chunk is under way while this one is worked on
+    float best = x[0];
+#pragma unroll
+    for (int j = 1; j < kLpEach; ++j) best = fmaxf(best, x[j]);
     const float m = fmaxf(st.m, best * kLog2e);
     if (m > st.m) {
       if (st.l != 0) {
-        const float d = st.m - m, f = __builtin_amdgcn_exp2f(d);
-        st.e = f == 0 ? 0.0f : f * (st.e + d * st.l);
+        const float s = st.m - m, f = __builtin_amdgcn_exp2f(s);
+        st.e = f == 0 ? 0.0f : f * (st.e + s * st.l);
         st.l *= f;
       }
       st.m = m;
     }
     const float ref = m == kLpNegInf ? 0.0f : m;
+    float e = st.e;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float d = fmaf(x[j], kLog2e, -ref);
-      const float q = __builtin_amdgcn_exp2f(d);
+    for (int j = 0; j < kLpEach; ++j) {
+      const float s = fmaf(x[j], kLog2e, -ref);
+      const float q = __builtin_amdgcn_exp2f(s);
       st.l += q;
-      st.e = fmaf(q, fmaxf(d, -256.0f), st.e);  // 2^d is 0 there: a logit of -inf adds 0, not NaN
+      e = fmaf(q, s, e);
     }
-    if (K && __ballot(top.n < K || best > top.cut)) lp_take<E>(top, x, K, lane, ids);
-  };
-  auto edge = [&](int from, int to) {  // fewer than 64 * E elements, one by one
-    float x[E];
+    if (e != e) {  // a logit of -inf (0 times -inf) or a NaN: once more, as -inf adds nothing
+      e = st.e;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int i = from + j * 64 + lane;
-      x[j] = i < to ? lp_value(row[i]) : kLpNegInf;
+      for (int j = 0; j < kLpEach; ++j) {
+        const float s = fmaf(x[j], kLog2e, -ref);
+        e = fmaf(__builtin_amdgcn_exp2f(s), fmaxf(s, -256.0f), e);
+      }
     }
-    add(x, [&](int j) { const int i = from + j * 64 + lane; return i < to ? i : -1; });
-  };
-  if (w == 0 && lead) edge(0, lead);
-  const T* const base = row + lead;
-  if (c0 < c1) {
-    TV buf[U], nxt[U];
-    auto load = [&](TV (&d)[U], int ch) {
+    st.e = e;
+    if (K && __ballot(top.n < K || best > lp_unkey(top.cut))) {
+      const T* const row = static_cast<const T*>(a.logits) + t0 * a.row_stride;
+      const int base = c0 * kLpChunk - lp_offset(row);
+      if (c0 == 0 || row_ends) {  // what lies outside the row is no element
+        best = __builtin_nanf("");
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        d[u] = *reinterpret_cast<const TV*>(base + static_cast<int64_t>(ch) * CHUNK + (u * 64 + lane) * VEC);
-    };
-    load(buf, c0);
-    for (int ch = c0; ch < c1; ++ch) {
-      if (ch + 1 < c1) load(nxt, ch + 1);
-      float x[E];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x[u * VEC + j] = lp_value(static_cast<T>(buf[u][j]));
-      const int first = lead + ch * CHUNK + lane * VEC;
-      add(x, [&](int j) { return first + (j / VEC) * 64 * VEC + j % VEC; });
-#pragma unroll
-      for (int u = 0; u < U; ++u) buf[u] = nxt[u];
+        for (int j = 0; j < kLpEach; ++j) {
+          const int id = base + lp_place<VEC>(j, lane);
+          x[j] = id >= 0 && id < V ? x[j] : __builtin_nanf("");
+          best = fmaxf(best, x[j]);
+        }
+      }
+      lp_take<VEC>(top, x, best, K, lane, base);
     }
-  }
-  if (w == waves - 1 && lead + chunks * CHUNK < V) edge(lead + chunks * CHUNK, V);
-
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const LpStat o{__shfl_xor(st.m, d), __shfl_xor(st.l, d), __shfl_xor(st.e, d)};
-    st = (lane & d) ? lp_join(o, st) : lp_join(st, o);
-  }
-  if (p.splits == 1) {
-    __shared__ float ss[kLpWaves][3], sv[kLpWaves * kTop];
-    __shared__ int si[kLpWaves * kTop];
-    if (lane == 0) ss[wave][0] = st.m, ss[wave][1] = st.l, ss[wave][2] = st.e;
-    if (lane < K) {
-      sv[wave * K + lane] = top.v;
-      si[wave * K + lane] = lane < top.n ? top.id : -1;
+    if (row_ends || left == 1) {
+      const LpStat s = lp_wave(st);
+      const int64_t at = w + t0;
+      if (lane == 0) {
+        p.stat[3 * at] = s.m;
+        p.stat[3 * at + 1] = s.l;
+        p.stat[3 * at + 2] = s.e;
+      }
+      if (lane < K) {
+        p.tk[at * K + lane] = lane < top.n ? top.k : kLpNone;
+        p.ti[at * K + lane] = top.id;
+      }
+      st = LpStat{kLpNegInf, 0, 0};
+      top = LpTop{};
     }
-    __syncthreads();
-    if (wave) return;
-    LpStat all;
-    LpTop best;
-    lp_join_parts(kLpWaves, K, lane, [&](int i) { return LpStat{ss[i][0], ss[i][1], ss[i][2]}; },
-                  [&](int i) { return sv[i]; }, [&](int i) { return si[i]; }, &all, &best);
-    lp_outputs<T>(a, t, all, best, lane);
-    return;
-  }
-  const int64_t at = static_cast<int64_t>(t) * waves + w;
-  if (lane == 0) {
-    p.stat[3 * at] = st.m;
-    p.stat[3 * at + 1] = st.l;
-    p.stat[3 * at + 2] = st.e;
-  }
-  if (lane < K) {
-    p.tv[at * K + lane] = top.v;
-    p.ti[at * K + lane] = lane < top.n ? top.id : -1;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(64) logprobs_join_kernel(verify_logprobs_args a, LpPlan p) {
   const int lane = threadIdx.x, t = blockIdx.x, K = a.top;
-  const int parts = p.splits * kLpWaves;
-  const int64_t at = static_cast<int64_t>(t) * parts;
-  LpStat all;
-  LpTop best;
-  lp_join_parts(parts, K, lane,
-                [&](int i) { return LpStat{p.stat[3 * (at + i)], p.stat[3 * (at + i) + 1], p.stat[3 * (at + i) + 2]}; },
-                [&](int i) { return p.tv[at * K + i]; }, [&](int i) { return p.ti[at * K + i]; }, &all, &best);
-  lp_outputs<T>(a, t, all, best, lane);
+  const T* const row = static_cast<const T*>(a.logits) + t * a.row_stride;
+  // The given tokens' logits, asked for first.
+  const int64_t tok0 = static_cast<int64_t>(t) * a.n_tokens;
+  auto token = [&](int n) {
+    return a.tokens_64 ? static_cast<const int64_t*>(a.tokens)[tok0 + n]
+                       : static_cast<int64_t>(static_cast<const int32_t*>(a.tokens)[tok0 + n]);
+  };
+  int64_t id0 = -1;
+  float x0 = 0;
+  if (lane < a.n_tokens) {
+    id0 = token(lane);
+    if (id0 >= 0 && id0 < a.vocab) x0 = static_cast<float>(row[id0]);
+  }
+
+  // The row's parts: of the waves from the one that has its first chunk to the one that has its last.
+  const int64_t w0 = static_cast<int64_t>(t) * p.chunks / p.per_wave;
+  const int64_t w1 = (static_cast<int64_t>(t + 1) * p.chunks - 1) / p.per_wave;
+  const int parts = static_cast<int>(w1 - w0 + 1);
+  const int64_t at0 = w0 + t;
+  LpStat st{kLpNegInf, 0, 0};
+  for (int i = lane; i < parts; i += 64)
+    st = lp_join(st, LpStat{p.stat[3 * (at0 + i)], p.stat[3 * (at0 + i) + 1], p.stat[3 * (at0 + i) + 2]});
+  st = lp_wave(st);
+  // The lists are sorted: the best of each first, then the second best, until none is good enough. All of
+  // 64 lists are asked for at once.
+  LpTop top;
+  for (int i0 = 0; i0 < parts && K; i0 += 64) {
+    const int i = i0 + lane;
+    int k[kTop], id[kTop];
+#pragma unroll
+    for (int r = 0; r < kTop; ++r) {
+      k[r] = kLpNone;
+      if (r < K && i < parts) {
+        k[r] = p.tk[(at0 + i) * K + r];
+        id[r] = p.ti[(at0 + i) * K + r];
+      }
+    }
+    int r0 = 0;
+    if (i0 == 0) {
+      lp_first(top, k[0], id[0], K, lane);
+      r0 = 1;
+    }
+#pragma unroll
+    for (int r = 0; r < kTop; ++r) {
+      if (r < r0 || r >= K) continue;
+      const uint64_t who = __ballot(k[r] != kLpNone && lp_good(top, k[r], id[r], K));
+      if (!who) break;
+      lp_each(top, who, k[r], id[r], K, lane);
+    }
+  }
+
+  const float lg = __builtin_amdgcn_logf(st.l);  // log2
+  const bool none = st.m == kLpNegInf && st.l == 0;  // every logit is -inf
+  const float z = kLn2 * (st.m + lg);
+  for (int n = lane; n < a.n_tokens; n += 64) {
+    if (n != lane) {
+      id0 = token(n);
+      if (id0 >= 0 && id0 < a.vocab) x0 = static_cast<float>(row[id0]);
+    }
+    a.logprobs[tok0 + n] = none || id0 < 0 || id0 >= a.vocab ? kLpNegInf : x0 - z;
+  }
+  if (a.entropy && lane == 0) a.entropy[t] = none ? 0.0f : kLn2 * (lg - st.e / st.l);
+  if (lane < K) {
+    const int64_t at = static_cast<int64_t>(t) * K + lane;
+    const bool there = lane < top.n;
+    a.top_ids[at] = there ? top.id : -1;
+    a.top_logprobs[at] = !there ? __builtin_nanf("") : none ? kLpNegInf : lp_unkey(top.k) - z;
+  }
 }
 
-// Blocks per row, and the workspace for the parts.
+// The cut of the rows into waves, and the workspace for the parts.
 inline LpPlan lp_plan(const verify_logprobs_args& a, void* workspace, int64_t* bytes) {
   LpPlan p{};
-  const int chunk = 64 * 16;  // logprobs_kernel's, either type
-  const int64_t most = (static_cast<int64_t>(a.vocab) / chunk + kLpWaves - 1) / kLpWaves;  // a chunk a wave
-  const int64_t want = (1024 + a.n_rows - 1) / a.n_rows;  // about four blocks a CU
-  int64_t s = want < most ? want : most;
-  p.splits = static_cast<int32_t>(s < 1 ? 1 : s);
-  const int64_t parts = static_cast<int64_t>(a.n_rows) * p.splits * kLpWaves;
-  *bytes = p.splits > 1 ? parts * (12 + 8 * a.top) : 0;
+  const int vec = a.type == VERIFY_F32 ? 4 : 8;
+  p.chunks = static_cast<int32_t>((static_cast<int64_t>(a.vocab) + vec - 1 + kLpChunk - 1) / kLpChunk);
+  const int64_t all = static_cast<int64_t>(a.n_rows) * p.chunks;
+  const int64_t resident = 256 * 4 * lp_waves(a.type == VERIFY_F32 ? 4 : 2);
+  p.per_wave = (all + resident - 1) / resident;
+  if (p.per_wave < 2) p.per_wave = 2;
+  p.waves = (all + p.per_wave - 1) / p.per_wave;
+  const int64_t parts = p.waves + a.n_rows;
+  *bytes = parts * (12 + 8 * a.top);
   p.stat = static_cast<float*>(workspace);
-  p.tv = p.stat + 3 * parts;
-  p.ti = reinterpret_cast<int32_t*>(p.tv + parts * a.top);
+  p.tk = reinterpret_cast<int32_t*>(p.stat + 3 * parts);
+  p.ti = p.tk + parts * a.top;
   return p;
 }
 
 template <typename T>
 hipError_t launch_logprobs_t(const verify_logprobs_args& a, const LpPlan& p, hipStream_t stream) {
-  logprobs_kernel<T><<<dim3(static_cast<unsigned>(p.splits) * a.n_rows), kLpThreads, 0, stream>>>(a, p);
+  logprobs_kernel<T><<<dim3(static_cast<unsigned>((p.waves + kLpWaves - 1) / kLpWaves)), kLpThreads, 0, stream>>>(a, p);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
+  if (e != hipSuccess) return e;
   logprobs_join_kernel<T><<<dim3(a.n_rows), 64, 0, stream>>>(a, p);
   return hipGetLastError();
 }

@@ -59,25 +59,37 @@ def _raise(status: int, what: str):
     raise MoeRoundError(status, what, _lib.verify_last_hip_error() if status == binding.ERR_HIP else 0)
 
 
+# The checks below run on every call of a round's hot path, so each takes the few attribute reads that tell
+# that all is well, and looks for what is wrong only if something is.
+
 def _tensor(t, name, device, dtypes, ndim):
+    """Checks t's kind; `device` is the index of the GPU that the call's tensors live on (-1: none)."""
+    try:
+        if t.dtype in dtypes and t.ndim == ndim and t.get_device() == device >= 0:
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.ndim != ndim:
         raise ValueError(f"{name}: {t.ndim} dimensions, not {ndim}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must live on the GPU, with the other tensors ({t.device}, {device})")
-    return t
+    raise ValueError(f"{name} must live on the GPU, with the other tensors ({t.device})")
 
 
 def _vector(t, name, device, length, dtype=torch.int32):
     _tensor(t, name, device, (dtype,), 1)
-    if t.shape[0] != length:
+    if t.size(0) != length:
         raise ValueError(f"{name}: length {t.shape[0]} != {length}")
-    if not t.is_contiguous():
+    if length > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _device(t):
+    """The index of the GPU that t lives on, -1 if on none (or no tensor: the checks say so)."""
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
 def _shape(t, name, shape):
@@ -89,9 +101,16 @@ def _strides(t, name):
     """Strides without the last dimension's, which must be contiguous.  A dimension of one element has
     no stride of its own (torch may report any): 0."""
     *outer, last = t.stride()
-    if last != 1 and t.shape[-1] > 1:
+    shape = t.shape
+    if last != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return [s if n > 1 else 0 for s, n in zip(outer, t.shape)]
+    if 1 in shape:
+        return [s if n > 1 else 0 for s, n in zip(outer, shape)]
+    return outer
+
+
+def _empty(device, dtype, *shape):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
 
 
 _I32 = (torch.int32,)
@@ -100,20 +119,17 @@ _CACHE = (torch.bfloat16, torch.float16)
 _ANY = (torch.float32, torch.bfloat16, torch.float16)
 
 
-def _on(device):
-    """The raw current stream of `device`; makes the device current for the call if it is not."""
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
-    return None, torch.cuda.current_stream(device).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
 def _call(fn, what, device, *args):
-    guard, stream = _on(device)
-    if guard is None:
-        st = fn(*args, stream)
+    """Calls the library on the current stream of `device`, which is made current if it is not."""
+    if device == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(device))
     else:
-        with guard:
-            st = fn(*args, stream)
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device))
     if st != OK:
         _raise(st, what)
 
@@ -143,7 +159,7 @@ def round_slots(cached: torch.Tensor, rows: torch.Tensor, table: torch.Tensor, f
     out             buffers of an earlier call with the same sizes, written again
     counts[0] <= N and counts[1] <= the free pages tell that everything fitted; what did not has slot -1.
     """
-    device = table.device if isinstance(table, torch.Tensor) else None
+    device = _device(table)
     _tensor(table, "table", device, _I32, 2)
     B, width = table.shape
     N = int(total_rows)
@@ -162,9 +178,9 @@ def round_slots(cached: torch.Tensor, rows: torch.Tensor, table: torch.Tensor, f
     hp = _vector(free_head, "free_head", device, 1) if free_head is not None else 0
     pp = _vector(parents, "parents", device, N) if parents is not None else 0
     if out is None:
-        buf = torch.empty(B + 3 + 2 * N, dtype=torch.int32, device=device)
+        buf = _empty(device, torch.int32, B + 3 + 2 * N)
         out = RoundSlots(buf[N + N:N + N + B + 1], buf[:N], buf[N:N + N],
-                         torch.empty(N, dtype=torch.int64, device=device) if parents is not None else None,
+                         _empty(device, torch.int64, N) if parents is not None else None,
                          buf[N + N + B + 1:])
     elif (out.masks is None) != (parents is None):
         raise ValueError("out.masks must be given exactly when parents are")
@@ -193,7 +209,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: t
     interleaved        rotates pairs (2i, 2i + 1) instead of (i, i + R/2)
     Returns q_out, [T, heads, D] of the cache's type (allocated if None; may be q itself).
     """
-    device = q.device if isinstance(q, torch.Tensor) else None
+    device = _device(q)
     _tensor(q, "q", device, _ANY, 3)
     T, heads, D = q.shape
     one = (q.dtype,)
@@ -210,7 +226,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: t
     if q.dtype != torch.float32 and q.dtype != k_cache.dtype:
         raise TypeError(f"q, k, v: dtype {q.dtype} is neither float32 nor the cache's {k_cache.dtype}")
     if q_out is None:
-        q_out = torch.empty((T, heads, D), dtype=k_cache.dtype, device=device)
+        q_out = _empty(device, k_cache.dtype, T, heads, D)
     else:
         _tensor(q_out, "q_out", device, (k_cache.dtype,), 3)
         _shape(q_out, "q_out", q.shape)
@@ -245,7 +261,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     Returns out, like q (allocated, as zeros, if None; may be q itself).  Rows that belong to no request
     are left as they were.
     """
-    device = q.device if isinstance(q, torch.Tensor) else None
+    device = _device(q)
     _tensor(q, "q", device, _CACHE, 3)
     T, heads, D = q.shape
     one = (q.dtype,)
@@ -259,7 +275,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if width > 1 and table.stride(1) != 1:
         raise ValueError("table: the last dimension must be contiguous")
     if out is None:
-        out = torch.zeros((T, heads, D), dtype=q.dtype, device=device)
+        out = _empty(device, q.dtype, T, heads, D).zero_()
     else:
         _tensor(out, "out", device, one, 3)
         _shape(out, "out", q.shape)
@@ -276,7 +292,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     need = lib.verify_tree_attention_workspace(args)
     if need < 0:
         _raise(need, "verify_tree_attention")
-    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    work = _empty(device, torch.uint8, need) if need else None
     _call(lib.verify_tree_attention, "verify_tree_attention", device, args,
           work.data_ptr() if need else None, need)
     return out
@@ -298,7 +314,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     tokens   [T, N] int32 or int64 (None: none); a token outside 0 .. V - 1 has log probability -inf
     top      alternatives per row, 0..min(V, 16), by descending logit, equal ones by ascending id
     """
-    device = logits.device if isinstance(logits, torch.Tensor) else None
+    device = _device(logits)
     _tensor(logits, "logits", device, _ANY, 2)
     T, V = logits.shape
     if V > 1 and logits.stride(1) != 1:
@@ -313,10 +329,10 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     if not 0 <= top <= MAX_ALTERNATIVES or top > V:
         raise ValueError(f"top must be between 0 and {min(V, MAX_ALTERNATIVES)}")
     lib = _load()
-    buf = torch.empty(T * (N + 1 + top), dtype=torch.float32, device=device)
+    buf = _empty(device, torch.float32, T * (N + 1 + top))
     logprobs, entropy = buf[:T * N].view(T, N), buf[T * N:T * N + T]
     top_logprobs = buf[T * N + T:].view(T, top)
-    top_ids = torch.empty((T, top), dtype=torch.int32, device=device)
+    top_ids = _empty(device, torch.int32, T, top)
     args = _LOGPROBS.pack(
         _LOGPROBS.size, logits.data_ptr(), tokens.data_ptr() if N else 0, logprobs.data_ptr() if N else 0,
         entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), logits.stride(0) if T > 1 else V,
@@ -324,6 +340,6 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     need = lib.verify_token_logprobs_workspace(args)
     if need < 0:
         _raise(need, "verify_token_logprobs")
-    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    work = _empty(device, torch.uint8, need) if need else None
     _call(lib.verify_token_logprobs, "verify_token_logprobs", device, args, work.data_ptr() if need else None, need)
     return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
