@@ -25,7 +25,19 @@ def lib():
     from verify_router_gemv_amd import build
     if not os.path.exists(binding.LIB_PATH):
         build.build()
-    return verify_ops._load()
+    verify_ops._native()
+    lib = binding.load()
+    args, vp, i64 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64
+    for name, res, sig in (
+            ("verify_round_slots", ctypes.c_int32, [args, vp]),
+            ("verify_qk_norm_rope", ctypes.c_int32, [args, vp]),
+            ("verify_tree_attention_workspace", i64, [args]),
+            ("verify_tree_attention", ctypes.c_int32, [args, vp, i64, vp]),
+            ("verify_token_logprobs_workspace", i64, [args]),
+            ("verify_token_logprobs", ctypes.c_int32, [args, vp, i64, vp]),
+            ("verify_last_hip_error", ctypes.c_int32, [])):
+        getattr(lib, name).restype, getattr(lib, name).argtypes = res, sig
+    return lib
 
 
 def declared():
@@ -38,18 +50,12 @@ def test_library_exports_exactly_the_declared_symbols(lib):
     assert sorted(l.split()[-1] for l in out.splitlines() if " T verify_" in l) == declared()
 
 
-# Field kinds of each struct in order (q = int64 or pointer, i = int32, f = float), names as in the header.
-FIELDS = {
-    "slots": (verify_ops._SLOTS, "verify_slots_args"),
-    "rope": (verify_ops._ROPE, "verify_rope_args"),
-    "attention": (verify_ops._ATTENTION, "verify_attention_args"),
-    "logprobs": (verify_ops._LOGPROBS, "verify_logprobs_args"),
-}
+STRUCTS = {k: f"verify_{k}_args" for k in ("slots", "rope", "attention", "logprobs")}
 
 
 def fields(kind):
     """(name, struct code) of the header's fields, read from its text."""
-    body = re.search(r"typedef struct %s \{(.*?)\} %s;" % ((FIELDS[kind][1],) * 2), open(HEADER).read(), re.S).group(1)
+    body = re.search(r"typedef struct %s \{(.*?)\} %s;" % ((STRUCTS[kind],) * 2), open(HEADER).read(), re.S).group(1)
     body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
     out = []
     for line in body.split(";"):
@@ -62,13 +68,13 @@ def fields(kind):
     return out
 
 
-@pytest.mark.parametrize("kind", FIELDS)
-def test_packed_structs_follow_the_header(kind):
-    packed = FIELDS[kind][0]
-    codes = "@" + "".join(c for _, c in fields(kind))
-    assert struct.calcsize(codes) == packed.size
-    ones = "".join(c * int(n or 1) for n, c in re.findall(r"(\d*)([a-zA-Z])", packed.format))
-    assert ones == codes[1:]
+def layout(kind):
+    """The struct's packing: the header's fields in order, each at its own alignment."""
+    return struct.Struct("@" + "".join(c for _, c in fields(kind)))
+
+
+def pack(kind, f):
+    return layout(kind).pack(*[f[n] for n, _ in fields(kind)])
 
 
 P16 = 0x100000   # a made-up aligned address: every check here comes before any GPU call
@@ -76,7 +82,7 @@ P16 = 0x100000   # a made-up aligned address: every check here comes before any 
 
 def base(kind):
     f = {n: P16 if c == "P" else 0 for n, c in fields(kind)}
-    f["struct_bytes"] = FIELDS[kind][0].size
+    f["struct_bytes"] = (layout(kind).size + 7) // 8 * 8
     if kind == "slots":
         f.update(n_requests=2, width=4, table_stride=4, n_free=3, page_size=16, total_rows=5)
     elif kind == "rope":
@@ -95,7 +101,7 @@ def base(kind):
 
 def call(lib, kind, **kw):
     f = {**base(kind), **kw}
-    args = FIELDS[kind][0].pack(*[f[n] for n, _ in fields(kind)])
+    args = pack(kind, f)
     if kind == "slots":
         return lib.verify_round_slots(args, None)
     if kind == "rope":
@@ -170,14 +176,14 @@ def test_null_structs_and_empty_calls(lib):
 def test_workspace_sizes(lib):
     def need(**kw):
         f = {**base("attention"), **kw}
-        return lib.verify_tree_attention_workspace(verify_ops._ATTENTION.pack(*[f[n] for n, _ in fields("attention")]))
+        return lib.verify_tree_attention_workspace(pack("attention", f))
     assert need(width=16) == 0            # 256 tokens: one part
     assert need(width=17) > 0
     assert need(n_rows=0) == 0 and need(scale=0.0) == INVALID
     f = base("logprobs")
-    pack = lambda **kw: verify_ops._LOGPROBS.pack(*[{**f, **kw}[n] for n, _ in fields("logprobs")])  # noqa: E731
-    assert lib.verify_token_logprobs_workspace(pack()) == 0
-    assert lib.verify_token_logprobs_workspace(pack(vocab=100000, row_stride=100000)) > 0
+    assert lib.verify_token_logprobs_workspace(pack("logprobs", f)) > 0
+    assert lib.verify_token_logprobs_workspace(pack("logprobs", {**f, "n_rows": 0})) == 0
+    assert lib.verify_token_logprobs_workspace(pack("logprobs", {**f, "vocab": 0})) == INVALID
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():
