@@ -92,8 +92,8 @@ def base(kind):
                  eps=1e-6)
     elif kind == "attention":
         f.update(q_row=512, q_head=128, o_row=512, o_head=128, kc_page=4096, kc_head=2048, kc_token=128, vc_page=4096,
-                 vc_head=2048, vc_token=128, table_stride=40, n_pages=7, n_rows=3, n_requests=2, heads=4, kv_heads=2,
-                 dim=128, page_size=16, width=40, max_rows=8, type=1, scale=0.1)
+                 vc_head=2048, vc_token=128, table_stride=90, n_pages=7, n_rows=3, n_requests=2, heads=4, kv_heads=2,
+                 dim=128, page_size=16, width=90, max_rows=8, type=1, scale=0.1)
     else:
         f.update(row_stride=1000, n_rows=3, vocab=1000, n_tokens=2, top=4, type=1)
     return f
@@ -137,7 +137,7 @@ BAD = [
     ("attention", dict(struct_bytes=1), INVALID), ("attention", dict(heads=3), INVALID), ("attention", dict(kv_heads=0), INVALID),
     ("attention", dict(width=0), INVALID), ("attention", dict(n_pages=0), INVALID), ("attention", dict(max_rows=0), INVALID),
     ("attention", dict(scale=0.0), INVALID), ("attention", dict(scale=-1.0), INVALID), ("attention", dict(scale=math.nan), INVALID),
-    ("attention", dict(scale=math.inf), INVALID), ("attention", dict(table_stride=39), INVALID),
+    ("attention", dict(scale=math.inf), INVALID), ("attention", dict(table_stride=89), INVALID),
     ("attention", dict(q=0), INVALID), ("attention", dict(out=P16 + 8), INVALID), ("attention", dict(masks=P16 + 4), INVALID),
     ("attention", dict(o_row=0), INVALID), ("attention", dict(kc_token=132), INVALID), ("attention", dict(table=0), INVALID),
     ("attention", dict(cached=0), INVALID), ("attention", dict(row_start=P16 + 2), INVALID),
@@ -177,8 +177,8 @@ def test_workspace_sizes(lib):
     def need(**kw):
         f = {**base("attention"), **kw}
         return lib.verify_tree_attention_workspace(pack("attention", f))
-    assert need(width=16) == 0            # 256 tokens: one part
-    assert need(width=17) > 0
+    assert need(width=64) == 0            # 1024 tokens: one part
+    assert need(width=65) > 0
     assert need(n_rows=0) == 0 and need(scale=0.0) == INVALID
     f = base("logprobs")
     assert lib.verify_token_logprobs_workspace(pack("logprobs", f)) > 0

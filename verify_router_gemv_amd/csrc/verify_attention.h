@@ -1,139 +1,154 @@
 // Attention of each request's tree of drafted rows over its paged cache.
 //
 // For one request and one kv head the M = rows * (heads / kv_heads) query rows share every key and
-// value, so a block holds all of them (up to 256) and streams the cache once.  Online softmax: with the
+// value, so a block holds up to 256 of them and streams the cache once.  Online softmax: with the
 // running maximum m, sum l and output O of the tokens so far, a tile of 32 tokens with scores s adds
 //   m' = max(m, max s), p = exp(s - m'), l' = l e^(m - m') + sum p, O' = O e^(m - m') + p V.
 //
-// Both products are 16x16x32 matrix instructions, computed transposed so that no operand crosses lanes:
-//   S^T (token x row)  = K Q^T : lane (c = lane % 16, g = lane / 16) loads 16 bytes of token c's key as it
-//                        lies in the cache; the result leaves it with row c's scores of tokens 4g..4g+3;
-//   O^T (value x row) += V^T P^T : the scores of the tile's two 16-token halves, rounded, ARE the lane's
-//                        part of P^T (the order of the 32 tokens along the reduction is free as long as
-//                        V^T follows it: tokens 4g..4g+3 of the first half, then of the second).  V^T needs
-//                        eight tokens of one value column in a lane: the lane loads columns 8c..8c+7 of
-//                        its eight tokens (whole 256-byte cache rows per load) and transposes the 8 x 8
-//                        block in its own registers; column 8c + i goes to the i-th product, which only
-//                        permutes the output's columns (undone by the store).
-// So keys and values go from memory to registers to the matrix cores, without LDS and without a
-// barrier in the loop; every wave has its own tokens (or, with many rows, its own rows) and loads a
-// tile ahead.
+// A wave holds 32 query rows and works on tiles of 32 tokens with 32x32x16 matrix instructions, both
+// products transposed so that no operand crosses lanes (c = lane % 32, h = lane / 32):
+//   S^T (token x row)  = K Q^T : lane (c, h) loads token c's key as it lies in the cache, 16 bytes a step;
+//                        the result leaves it with row c's scores of tokens 8q + 4h + r (q, r < 4);
+//   O^T (value x row) += V^T P^T : the lane's 16 probabilities, rounded, ARE its part of P^T (the order of
+//                        the tokens along the reduction is free as long as V^T follows it).  V^T needs
+//                        eight tokens of one value column in a lane: the lane loads D / 32 neighbouring
+//                        columns of its own 16 tokens (whole cache rows per load) and transposes them in
+//                        its own registers; its i-th column goes to the i-th product, which only permutes
+//                        the output's columns (undone by the store).
+// A tile goes from memory straight into LDS (loads that write LDS, 16 bytes a lane), some tiles ahead of its
+// use, and from there into the operands.  The waves of a block split the rows (WM) and the tokens (WK):
+// the WM waves of a token stream share its tiles and fetch a part of each; a stream has as many stages as
+// LDS holds (1 with WM = 1: the wave takes the tile into registers and refills the stage while it works).
+// Keys lie in LDS with their 16-byte pieces exchanged within the token (piece ^ token), so that the reads of
+// 32 tokens' same piece hit different banks; values as they are.
 //
-// The context is split over blocks: the blocks that fit on the chip at once are handed out by
-// rows * tokens of each request (computed by every block from the lengths, see AttnPlan), and a second
-// kernel joins the parts of requests with more than one.
-// Bound: memory (each K/V byte is read once) up to about 64 query rows a kv head; above, the matrix
-// cores and the exponentials.
+// The context is split over blocks: the blocks that the chip holds at once are handed out by
+// rows * tokens of each request (worked out by every block from the lengths), and a second kernel joins
+// the parts of requests with more than one.
+// Bound: memory (each K/V byte is read once) up to about 64 query rows a kv head; above, the
+// exponentials and the matrix cores.
 #pragma once
 
 #include "verify_common.h"
 
 namespace verify {
 
-constexpr int kAttnThreads = 256;
 constexpr int kTile = 32;          // tokens per step of a wave
-constexpr int kMinChunk = 256;     // fewest tokens a block is split down to
+constexpr int kMinTiles = 4;       // fewest tiles per wave a context is split down to
+constexpr int kCus = 256;
 constexpr float kNegInf = -__builtin_inff();
 
-// How the work of one call is cut up. The host fixes `target` (blocks that may be resident) and the
-// grid from the sizes it knows; the rest follows from the lengths on the GPU, the same in every block.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// How the work of one call is cut up. The host fixes `target` and the grid from the sizes it knows; the
+// rest follows from the lengths on the GPU, the same in every block.
 struct AttnLaunch {
-  int32_t m_block;   // query rows (rows * group) per block
+  int32_t m_shift;   // log2 of the query rows (rows * group) per block
   int32_t target;    // blocks to spread the work over, all heads together
   int32_t grid;      // blocks launched
+  int32_t least;     // fewest tiles of a part
   int32_t swizzle;   // 1: several row blocks per request, kept on one XCD (8 neighbours)
-  float* part;       // [grid][m_block][D] partial outputs, then [grid][m_block][2] (maximum, sum)
+  float* part;       // [grid][rows][D] partial outputs, then [grid][rows][2] (maximum, sum)
+  int32_t* plan;     // [B][2] first block and number of parts of each request, for the join
 };
 
-struct AttnItem {
-  int b, rows, start;       // request, its rows, its first row
-  int cached, len;          // tokens before the round, tokens in all
-  int chunk, chunks;        // this block's part of the context, of how many
-  int mb, head;             // this block's row block and kv head
-  int first;                // index of the request's first block
+struct AttnRequest {
+  int start, rows, cached, len;  // first row, rows, tokens before the round, tokens in all
 };
 
-template <typename A>
-__device__ __forceinline__ void attn_request(const A& a, int b, int* start, int* rows, int* cached, int* len) {
+__device__ __forceinline__ AttnRequest attn_request(const verify_attention_args& a, int b) {
   int s = a.row_start[b], e = a.row_start[b + 1];
-  s = s < 0 ? 0 : s > a.n_rows ? a.n_rows : s;
-  e = e < s ? s : e > a.n_rows ? a.n_rows : e;
-  int r = e - s;
-  r = r > a.max_rows ? a.max_rows : r;
-  const int64_t most = static_cast<int64_t>(a.width) * a.page_size;  // tokens the table can hold
-  int64_t c = max0(a.cached[b]);
-  c = c < most ? c : most;
-  int64_t n = c + r;
-  n = n < most ? n : most;
-  *start = s;
-  *rows = r;
-  *cached = static_cast<int>(c);
-  *len = static_cast<int>(n);
+  int c = a.cached[b];
+  s = min(max(s, 0), a.n_rows);
+  e = min(max(e, s), a.n_rows);
+  const int r = min(e - s, a.max_rows);
+  const int most = a.width * a.page_size;  // tokens the table can hold, at most 2^30
+  c = min(max(c, 0), most);
+  return {s, r, c, min(c + r, most)};
 }
 
-// Tokens per block so that the whole call makes about `target` blocks.
-__device__ __forceinline__ int attn_chunk(const verify_attention_args& a, const AttnLaunch& p, int lane) {
-  const int group = a.heads / a.kv_heads;
-  int64_t work = 0;
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+  auto up = [&](int w, auto ctrl) {
+    return static_cast<int>(moe::dpp_u32<decltype(ctrl)::value>(static_cast<uint32_t>(w)));
+  };
+  // within rows of 16 lanes (lanes shifted in from outside the row are 0), then the rows' totals
+  v += up(v, std::integral_constant<int, 0x111>{});
+  v += up(v, std::integral_constant<int, 0x112>{});
+  v += up(v, std::integral_constant<int, 0x114>{});
+  v += up(v, std::integral_constant<int, 0x118>{});
+  const int t0 = __builtin_amdgcn_readlane(v, 15), t1 = __builtin_amdgcn_readlane(v, 31),
+            t2 = __builtin_amdgcn_readlane(v, 47);
+  return v + (lane >= 16 ? t0 : 0) + (lane >= 32 ? t1 : 0) + (lane >= 48 ? t2 : 0);
+}
+
+// The request, row block, kv head and part of the context that block `at` works on; false: none. Called
+// by all lanes of a wave.
+struct AttnItem {
+  AttnRequest q;
+  int b, mb, head, part, parts;
+};
+
+__device__ __forceinline__ bool attn_item(const verify_attention_args& a, const AttnLaunch& p, int lane, int group,
+                                          int at, AttnItem* it) {
+  const int rnd = (1 << p.m_shift) - 1;
+  // Tiles per block so that the whole call makes about `target` blocks. (As float: rounding moves the
+  // cut, alike in all blocks, and the grid has blocks to spare.)
+  float work = 0;
+  AttnRequest q{0, 0, 0, 0};
   for (int b = lane; b < a.n_requests; b += 64) {
-    int s, r, c, n;
-    attn_request(a, b, &s, &r, &c, &n);
-    work += static_cast<int64_t>((r * group + p.m_block - 1) / p.m_block) * n;
+    q = attn_request(a, b);
+    work += static_cast<float>((q.rows * group + rnd) >> p.m_shift) * static_cast<float>((q.len + kTile - 1) / kTile);
   }
-  work = wave_sum64(work) * a.kv_heads;
-  int64_t c = (work + p.target - 1) / p.target;
-  c = (c + kTile - 1) / kTile * kTile;
-  c = c < kMinChunk ? kMinChunk : c;
-  return c < INT32_MAX / 2 ? static_cast<int>(c) : INT32_MAX / 2;
-}
-
-// Blocks of one request: row blocks x kv heads x chunks, the last two rounded up together to a multiple
-// of 8 when there are several row blocks.
-__device__ __forceinline__ int attn_blocks(const verify_attention_args& a, const AttnLaunch& p, int rows, int len,
-                                           int chunk, int* chunks) {
-  const int mbs = (rows * (a.heads / a.kv_heads) + p.m_block - 1) / p.m_block;
-  const int n = len > chunk ? (len + chunk - 1) / chunk : 1;
-  *chunks = n;
-  int u = n * a.kv_heads;
-  if (p.swizzle) u = (u + 7) & ~7;
-  return mbs * u;
-}
-
-// The request that block `at` works on (want_b < 0), or the plan of request want_b. False: none.
-__device__ __forceinline__ bool attn_find(const verify_attention_args& a, const AttnLaunch& p, int lane, int at,
-                                          int want_b, AttnItem* it) {
-  const int chunk = attn_chunk(a, p, lane);
-  int64_t base = 0;
+  work = wave_sum(work) * static_cast<float>(a.kv_heads);
+  const float c = ceilf(work / static_cast<float>(p.target));
+  const unsigned chunk = max(static_cast<unsigned>(c), static_cast<unsigned>(p.least));
+  int base = 0;
   for (int b0 = 0; b0 < a.n_requests; b0 += 64) {
     const int b = b0 + lane;
-    int s = 0, r = 0, c = 0, n = 0, chunks = 1, blocks = 0;
-    if (b < a.n_requests) {
-      attn_request(a, b, &s, &r, &c, &n);
-      blocks = r ? attn_blocks(a, p, r, n, chunk, &chunks) : 0;
-    }
-    const int64_t end = base + wave_scan64(blocks, lane);
-    const uint64_t hit = want_b >= 0 ? (want_b - b0 < 64 ? uint64_t(1) << (want_b - b0) : 0) : __ballot(end > at);
+    if (a.n_requests > 64) q = b < a.n_requests ? attn_request(a, b) : AttnRequest{0, 0, 0, 0};
+    const unsigned tiles = static_cast<unsigned>(q.len + kTile - 1) / kTile;
+    const int parts = tiles > chunk ? static_cast<int>((tiles + chunk - 1) / chunk) : 1;
+    const int mbs = (q.rows * group + rnd) >> p.m_shift;
+    int units = parts * a.kv_heads;
+    if (p.swizzle) units = (units + 7) & ~7;
+    const int blocks = mbs * units;
+    const int end = base + wave_scan(blocks, lane);
+    const uint64_t hit = __ballot(end > at);
     if (hit) {
       const int from = __ffsll(static_cast<unsigned long long>(hit)) - 1;
       it->b = b0 + from;
-      it->start = uniform(__shfl(s, from));
-      it->rows = uniform(__shfl(r, from));
-      it->cached = uniform(__shfl(c, from));
-      it->len = uniform(__shfl(n, from));
-      it->chunks = uniform(__shfl(chunks, from));
-      const int last = uniform(__shfl(static_cast<int>(end), from));  // blocks fit 31 bits (checked by the host)
-      it->first = last - uniform(__shfl(blocks, from));
-      return true;
+      it->q.start = __builtin_amdgcn_readlane(q.start, from);
+      it->q.rows = __builtin_amdgcn_readlane(q.rows, from);
+      it->q.cached = __builtin_amdgcn_readlane(q.cached, from);
+      it->q.len = __builtin_amdgcn_readlane(q.len, from);
+      it->parts = __builtin_amdgcn_readlane(parts, from);
+      const int n_mb = __builtin_amdgcn_readlane(mbs, from);
+      const int first = __builtin_amdgcn_readlane(end - blocks, from);
+      // A request's blocks in launch order: (part, head) units; with the swizzle in groups of 8, row blocks
+      // in between, so that the row blocks of one unit are 8 apart and reach the same XCD (and its L2).
+      int unit = at - first;
+      it->mb = 0;
+      if (p.swizzle) {
+        const int group8 = unit / (8 * n_mb), r = unit - group8 * 8 * n_mb;
+        it->mb = r >> 3;
+        unit = group8 * 8 + (r & 7);
+      }
+      if (p.plan && unit == 0 && it->mb == 0 && threadIdx.x == 0) {
+        p.plan[2 * it->b] = first;
+        p.plan[2 * it->b + 1] = it->parts;
+      }
+      it->part = unit / a.kv_heads;
+      it->head = unit - it->part * a.kv_heads;
+      return it->part < it->parts;  // the swizzle's rounding
     }
-    base += __shfl(end - base, 63);
+    base = __builtin_amdgcn_readlane(end, 63);
   }
   return false;
 }
 
-// A request's blocks in launch order: with the swizzle, groups of 8 (chunk, head) units, row blocks in
-// between, so that the row blocks of one unit are 8 apart and reach the same XCD (and its L2).
-__device__ __forceinline__ int attn_unit_block(const AttnLaunch& p, int unit, int mb, int mbs) {
-  return p.swizzle ? (unit >> 3) * 8 * mbs + mb * 8 + (unit & 7) : unit;
+__device__ __forceinline__ int64_t attn_slot(const AttnLaunch& p, int first, int unit, int mb, int mbs) {
+  return first + (p.swizzle ? (unit >> 3) * 8 * mbs + mb * 8 + (unit & 7) : unit);
 }
 
 template <typename T>
@@ -141,390 +156,398 @@ struct Mfma;
 template <>
 struct Mfma<__bf16> {
   typedef bf16x8 V;
-  static __device__ __forceinline__ f32x4 mul(V a, V b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  static __device__ __forceinline__ f32x16 mul(V a, V b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  static constexpr uint32_t kExp = 0x7f80;  // the exponent bits: all set in infinities and NaN
+  // A half word's exponent bits are all set (infinity, NaN) when this step carries into its top bit.
+  static constexpr uint32_t kExp = 0x7f807f80, kExpStep = 0x00800080;
   static constexpr float kLift = 0.0f;
 };
 template <>
 struct Mfma<_Float16> {
   typedef f16x8 V;
-  static __device__ __forceinline__ f32x4 mul(V a, V b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  static __device__ __forceinline__ f32x16 mul(V a, V b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  static constexpr uint32_t kExp = 0x7c00;
+  static constexpr uint32_t kExp = 0x7c007c00, kExpStep = 0x04000400;
   // Probabilities are held 2^7 times as large (a factor of the sums too, so it cancels): up to 2^15, below
   // the type's largest value, and 2^-21 of the running maximum still has the type's full precision.
   static constexpr float kLift = 7.0f;
 };
 
-// Maximum / sum over the lanes that hold the other tokens of the same query row.
-__device__ __forceinline__ float rows_max(float v) {
-  const float2 a = across<16>(v);
-  const float2 b = across<32>(fmaxf(a.x, a.y));
-  return fmaxf(b.x, b.y);
+// With the lane that holds the other half of a row's tokens.
+__device__ __forceinline__ float row_max(float v) {
+  const float2 a = across<32>(v);
+  return fmaxf(a.x, a.y);
 }
-__device__ __forceinline__ float rows_sum(float v) {
-  const float2 a = across<16>(v);
-  const float2 b = across<32>(a.x + a.y);
-  return b.x + b.y;
+__device__ __forceinline__ float row_sum(float v) {
+  const float2 a = across<32>(v);
+  return a.x + a.y;
 }
 
-// One wave's view of the tile of 32 tokens at `tok`: its keys (16-byte pieces) and values.
-template <int D>
-struct KV {
-  static constexpr int KK = D / 32;            // matrix steps along the head
-  static constexpr int VW = D == 64 ? 2 : 4;   // dwords of a value load (D = 64: 4 columns per lane)
-  static constexpr int VH = D == 256 ? 2 : 1;  // 128-column halves
-  u32x4 k[2][KK];
-  uint32_t v[8][VH][VW];
-  bool ok[2];                                  // the half tile's page exists
-};
+// Which of the four tokens at `at` .. `at` + 3 a row sees, as bits: all before `cached`, drafted ones by the
+// row's mask, none from `end` on.
+__device__ __forceinline__ uint32_t attn_seen(int at, int cached, int end, uint64_t mask) {
+  const int d = at - cached;
+  const uint32_t past = static_cast<uint32_t>(mask << min(max(-d, 0), 3)) | ((1u << min(max(-d, 0), 4)) - 1u);
+  const uint32_t bits = d < 0 ? past : d < 64 ? static_cast<uint32_t>(mask >> (d & 63)) : 0u;
+  return bits & ((1u << min(max(end - at, 0), 4)) - 1u);
+}
 
-template <typename T, int D, int NM, int WK>
-__global__ void __launch_bounds__(kAttnThreads) attn_kernel(verify_attention_args a, AttnLaunch p) {
+template <typename T, int D, int WM, int WK>
+__global__ void __launch_bounds__(64 * WM * WK, D == 256 ? 1 : 2)
+attn_kernel(verify_attention_args a, AttnLaunch p) {
   typedef Mfma<T> MM;
   typedef typename MM::V V8;
-  typedef KV<D> Tile;
-  constexpr int KK = Tile::KK, VW = Tile::VW, VH = Tile::VH, DV = 2 * VW;  // DV columns of a lane per half
-  constexpr int NT = VH * DV;                                              // output tiles (16 columns each)
-  constexpr int WM = 4 / WK, MB = 16 * NM * WM;
+  constexpr int KK = D / 16;          // matrix steps along the head
+  constexpr int DV = D / 32;          // value columns of a lane
+  constexpr int VW = DV / 2;          // their dwords
+  constexpr int MB = 32 * WM, NT = 64 * WM * WK;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int c = lane & 15, g = lane >> 4;
+  const int c = lane & 31, h = lane >> 5;
   const int wk = wave % WK, wm = wave / WK;
   const int group = a.heads / a.kv_heads;
 
   AttnItem it;
-  if (!attn_find(a, p, lane, blockIdx.x, -1, &it)) return;
-  const int mbs = (it.rows * group + MB - 1) / MB;
-  int unit;
-  {
-    const int at = blockIdx.x - it.first;
-    if (p.swizzle) {
-      const int q = at / (8 * mbs), r = at - q * 8 * mbs;
-      it.mb = r >> 3;
-      unit = q * 8 + (r & 7);
-    } else {
-      it.mb = 0;
-      unit = at;
-    }
-    if (unit >= it.chunks * a.kv_heads) return;  // rounding of the swizzle
-    it.head = unit % a.kv_heads;
-    it.chunk = unit / a.kv_heads;
-  }
-  // Chunks of equal length, whole tiles.
-  const int step = ((it.len + it.chunks - 1) / it.chunks + kTile - 1) / kTile * kTile;
-  const int t0 = it.chunk * step;
-  const int t1 = t0 + step < it.len ? t0 + step : it.len;
+  if (!attn_item(a, p, lane, group, blockIdx.x, &it)) return;
+  // Parts of equal length, whole tiles.
+  const int tiles = (it.q.len + kTile - 1) / kTile;
+  const int each = (tiles + it.parts - 1) / it.parts;
+  const int t0 = it.part * each * kTile;
+  const int t1 = min(t0 + each * kTile, it.q.len);
 
-  // Query rows: row m = 16 (NM wm + n) + c of the block, in the order of the matrix operand.
-  V8 q[NM][KK];
-  uint64_t mask[NM];
-  const int m0 = it.mb * MB + wm * 16 * NM;
-  const int total = it.rows * group;
-  const uint64_t inside = it.rows >= 64 ? ~uint64_t(0) : (uint64_t(1) << it.rows) - 1;
-#pragma unroll
-  for (int n = 0; n < NM; ++n) {
-    const int m = m0 + 16 * n + c;
-    const int mm = m < total ? m : 0;
-    const int i = mm / group, h = it.head * group + (mm - i * group);
-    const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(it.start + i) * a.q_row + h * a.q_head + 8 * g;
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) q[n][kk] = *reinterpret_cast<const V8*>(src + 32 * kk);
-    mask[n] = a.masks ? static_cast<uint64_t>(a.masks[it.start + i]) : (uint64_t(2) << i) - 1;
-    mask[n] &= inside;
-  }
-
-  f32x4 o[NM][NT] = {};
-  float mx[NM], sum[NM];  // running maximum of the raw scores, sum of the lane's own probabilities
-#pragma unroll
-  for (int n = 0; n < NM; ++n) mx[n] = kNegInf, sum[n] = 0;
+  f32x16 o[DV] = {};
+  float mx = kNegInf, sum = 0;  // running maximum of the raw scores, sum of the lane's own probabilities
   const float sc = a.scale * 1.4426950408889634f;  // exponentials are powers of two
 
   const int shift = __builtin_ctz(a.page_size), in_page = a.page_size - 1;
   const int32_t* const pages = a.table + it.b * a.table_stride;
-  const T* const kbase = static_cast<const T*>(a.k_cache) + it.head * a.kc_head;
-  const T* const vbase = static_cast<const T*>(a.v_cache) + it.head * a.vc_head;
+  const char* const kbase = static_cast<const char*>(a.k_cache) + it.head * a.kc_head * 2;
+  const char* const vbase = static_cast<const char*>(a.v_cache) + it.head * a.vc_head * 2;
+  const uint32_t k_token = static_cast<uint32_t>(a.kc_token) * 2, v_token = static_cast<uint32_t>(a.vc_token) * 2;
+
   // 16 tokens never cross a page. A page past the table or the cache is not read: its tokens count as
   // unseen (page 0 is read instead, and dropped).
   auto page_of = [&](int tok) {
     const int col = tok >> shift;
-    const int page = col < a.width ? pages[col] : -1;
+    const int page = tok < t1 && col < a.width ? pages[col] : -1;
     return page < a.n_pages ? page : -1;
   };
-  auto load = [&](Tile& x, int tok, const int (&page)[2]) {
+
+  // A stage: 32 tokens' keys, then their values, 2 D bytes a token. One load of a wave writes 1 KB of it,
+  // lane l the 16 bytes at 16 l: whole tokens, CR lanes each.
+  constexpr int CR = D / 8, RB = 2 * D, KI = D / 16;  // pieces and bytes of a token; loads of the keys
+  constexpr int NI = 2 * KI / WM;                     // loads of a wave per tile
+  constexpr uint32_t kStage = 2 * kTile * RB;
+  constexpr int NS = WM == 1 ? 1 : WM == 2 ? 2 : 4;   // stages of a stream
+  constexpr int LD = D + 4;                           // padded row of the waves' outputs, joined at the end
+  constexpr uint32_t kOut = WK > 1 ? WM * WK * 32 * (LD + 2) * 4 : 0;
+  __shared__ __align__(1024) char lds[WK * NS * kStage > kOut ? WK * NS * kStage : kOut];
+  char* const stream = lds + wk * NS * kStage;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) char*)stream));
+  auto twist = [](int token) { return (D == 64 ? token >> 1 : token) & (CR < 16 ? CR - 1 : 15); };
+  const int lr = lane / CR, lc = lane % CR;           // a load's token and piece of this lane
+  const uint32_t k_lane = lr * k_token, v_lane = lr * v_token + 16 * lc;
+  const int k_piece = lc ^ twist(lr);
+  auto tok_of = [&](int tile) { return t0 + (tile * WK + wk) * kTile; };
+  // Lane i: the page of half i % 2 of the tile i / 2 after the last multiple of 32 (looked up 32 tiles at a
+  // time, so that the loop waits for nothing but its tiles).
+  int page_list = 0;
+  auto look_up = [&](int tile) {
+    page_list = page_of(tok_of(tile + (lane >> 1)) + 16 * (lane & 1));
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  };
+  uint32_t lost = 0;          // two bits a tile in flight, the one in use lowest: its halves without a page
+  auto ask = [&](int tile) {  // the wave's loads of a tile
+    const int tok = tok_of(tile);
+    if ((tile & 31) == 0) look_up(tile);
+    const int page0 = __builtin_amdgcn_readlane(page_list, 2 * (tile & 31));
+    const int page1 = __builtin_amdgcn_readlane(page_list, 2 * (tile & 31) + 1);
+    const int pg0 = max(page0, 0), pg1 = max(page1, 0);
+    const uint32_t to = lds0 + (NS > 1 ? tile % NS * kStage : 0);
+    const int place = tok & in_page, place1 = (tok + 16) & in_page;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      x.ok[s] = page[s] >= 0;
-      const int64_t pg = page[s] >= 0 ? page[s] : 0;
-      const int place = (tok + 16 * s) & in_page;
-      const T* kp = kbase + pg * a.kc_page + place * a.kc_token + (c * static_cast<int>(a.kc_token) + 8 * g);
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) x.k[s][kk] = *reinterpret_cast<const u32x4*>(kp + 32 * kk);
-      const T* vp = vbase + pg * a.vc_page + place * a.vc_token;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int hv = 0; hv < VH; ++hv) {
-          const T* src = vp + ((4 * g + j) * static_cast<int>(a.vc_token) + DV * c + 128 * hv);
-          if constexpr (VW == 4) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(src);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x.v[4 * s + j][hv][e] = w[e];
-          } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(src);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x.v[4 * s + j][hv][e] = w[e];
-          }
-        }
+    for (int j = 0; j < NI; ++j) {
+      const int n = j * WM + wm;
+      const bool is_k = n < KI;
+      const int row = (is_k ? n : n - KI) * (512 / D);
+      const int64_t pg = row < 16 ? pg0 : pg1;
+      const uint32_t at = (row < 16 ? place : place1) + (row & 15);
+      const char* const src = is_k ? kbase + pg * (a.kc_page * 2) + static_cast<uint64_t>(at) * k_token
+                                   : vbase + pg * (a.vc_page * 2) + static_cast<uint64_t>(at) * v_token;
+      const uint32_t off = is_k ? k_lane + 16 * (k_piece ^ twist(row)) : v_lane;
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                   :: "s"(to + n * 1024), "v"(off), "s"(src) : "memory");
     }
+    lost |= ((page0 < 0 ? 1u : 0u) | (page1 < 0 ? 2u : 0u)) << (2 * (NS > 1 ? NS - 1 : 0));
   };
 
-  auto compute = [&](Tile& x, int tok) {
-    const bool edge = tok + kTile > it.cached || !x.ok[0] || !x.ok[1];  // some token may be unseen
-    f32x4 s[NM][2] = {};
+  // Tiles of the stream with the most of them: all waves of the block go round as often.
+  const int all = (max(t1 - t0, 0) + kTile - 1) / kTile;
+  const int rounds = (all + WK - 1) / WK, mine = (all - wk + WK - 1) / WK;
+  if constexpr (NS == 1) {
+    if (mine > 0) ask(0);
+  } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < NS - 1; ++i) {
+      if (i < mine) ask(i);
+      lost >>= 2;
+    }
+  }
+  // Query rows: row m = 32 wm + c of the block, in the order of the matrix operand.
+  V8 q[KK];
+  uint64_t mask;
+  const int total = it.q.rows * group;
+  {
+    const int m = (it.mb << p.m_shift) + wm * 32 + c;
+    const int mm = m < total ? m : 0;
+    const int i = mm / group, hq = it.head * group + (mm - i * group);
+    const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(it.q.start + i) * a.q_row + hq * a.q_head + 8 * h;
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
+    for (int kk = 0; kk < KK; ++kk) q[kk] = *reinterpret_cast<const V8*>(src + 16 * kk);
+    mask = a.masks ? static_cast<uint64_t>(a.masks[it.q.start + i]) : (uint64_t(2) << i) - 1;
+    if (it.q.rows < 64) mask &= (uint64_t(1) << it.q.rows) - 1;
+  }
+  // Waited for here, as the compiler would in every round of the loop, and for all that is asked there too.
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+
+  const int k_row = c * RB, k_twist = h ^ twist(c);
+  const int v_row = kTile * RB + 4 * h * RB + 2 * DV * c;
+
+  for (int tile = 0; tile < rounds; ++tile) {
+    const int tok = tok_of(tile);
+    if constexpr (NS == 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    } else {
+      // The tile has arrived when at most the loads of the NS - 2 tiles after it are still under way; every
+      // wave has also finished with the stage that is asked for next.
+      if (tile + NS - 2 < mine) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"((NS - 2) * NI) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      asm volatile("s_barrier" ::: "memory");
+      if (tile + NS - 1 < mine) ask(tile + NS - 1);
+    }
+    if (tile >= mine) {
+      if constexpr (NS == 1) break;
+      continue;
+    }
+    const char* const at0 = stream + (NS > 1 ? tile % NS * kStage : 0);
+    u32x4 k[KK];
+    uint32_t v[16][VW];
 #pragma unroll
-        for (int n = 0; n < NM; ++n)
-          s[n][h] = MM::mul(__builtin_bit_cast(V8, x.k[h][kk]), q[n][kk], s[n][h]);
-    bool slow = false;
+    for (int kk = 0; kk < KK; ++kk) k[kk] = *reinterpret_cast<const u32x4*>(at0 + k_row + 16 * (2 * kk ^ k_twist));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const char* const src = at0 + v_row + (8 * (j >> 2) + (j & 3)) * RB;
+      if constexpr (VW == 4) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(src);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][e] = w[e];
+      } else if constexpr (VW == 2) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(src);
+        v[j][0] = w[0], v[j][1] = w[1];
+      } else {
+        v[j][0] = *reinterpret_cast<const uint32_t*>(src);
+      }
+    }
+    const bool lost0 = lost & 1, lost1 = lost & 2;
+    lost >>= 2;
+    if constexpr (NS == 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (tile + 1 < mine) ask(tile + 1);
+    }
+    f32x16 s = {};
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) s = MM::mul(__builtin_bit_cast(V8, k[kk]), q[kk], s);
+
+    const bool edge = tok + kTile > it.q.cached || lost0 || lost1;  // some token may be unseen
+    uint32_t bad = 0;
     if (edge) {
       // Scores of unseen tokens are replaced, whatever they are; values of tokens that nobody may see
-      // (past the end, on no page) are zeroed, and a drafted token's infinity or NaN is kept out of the
-      // matrix product, which would spread it to the rows that do not see the token.
-      uint32_t bad = 0;
+      // (past the end, on no page) are zeroed, and a drafted token's infinity or NaN is found, which the
+      // matrix product would spread to the rows that do not see the token.
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int j = 0; j < 4; ++j) {
+        const int at = tok + 8 * j + 4 * h;
+        const int end = (j < 2 ? lost0 : lost1) ? at : t1;
+        const uint32_t bits = attn_seen(at, it.q.cached, end, mask);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int t = tok + 16 * h + 4 * g + r, d = t - it.cached;
-          const bool real = x.ok[h] && t < t1;
+          s[4 * j + r] = (bits >> r) & 1 ? s[4 * j + r] : kNegInf;
+          const bool real = at + r < end, drafted = at + r >= it.q.cached;
 #pragma unroll
-          for (int n = 0; n < NM; ++n) {
-            const bool seen = real && (d < 0 || (d < 64 && ((mask[n] >> (d & 63)) & 1)));
-            s[n][h][r] = seen ? s[n][h][r] : kNegInf;
+          for (int e = 0; e < VW; ++e) {
+            const uint32_t w = real ? v[4 * j + r][e] : 0;
+            v[4 * j + r][e] = w;
+            bad |= drafted ? (w & MM::kExp) + MM::kExpStep : 0;
           }
-#pragma unroll
-          for (int hv = 0; hv < VH; ++hv)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              uint32_t w = real ? x.v[4 * h + r][hv][e] : 0;
-              if (d >= 0) {
-                const bool lo = (w & MM::kExp) == MM::kExp;
-                const bool hi = ((w >> 16) & MM::kExp) == MM::kExp;
-                bad |= lo | hi;
-                w = (lo ? 0 : w & 0xffffu) | (hi ? 0 : w & 0xffff0000u);
-              }
-              x.v[4 * h + r][hv][e] = w;
-            }
         }
-      slow = __ballot(bad) != 0;
+      }
+      bad = __ballot((bad & 0x80008000u) != 0) != 0;
+      if (bad) {  // keep them out of the product
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            const uint32_t w = v[j][e];
+            const uint32_t x = (w & MM::kExp) + MM::kExpStep;
+            const bool drafted = tok + 8 * (j >> 2) + 4 * h + (j & 3) >= it.q.cached;
+            if (drafted) v[j][e] = (x & 0x8000u ? 0 : w & 0xffffu) | (x & 0x80000000u ? 0 : w & 0xffff0000u);
+          }
+      }
     }
     // Probabilities relative to a running maximum that a row raises only when its own grows by more than
     // 8 powers of two: until then p <= 2^8, which both 16-bit types hold with their full precision. (Each
     // row by itself: its result does not depend on the other rows' values.)
-    float raised[NM];
-    bool grow = false;
+    float top = fmaxf(fmaxf(s[0], s[1]), s[2]);
 #pragma unroll
-    for (int n = 0; n < NM; ++n) {
-      float v = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                      fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-      v = rows_max(v);
-      const bool up = (v - mx[n]) * sc > 8.0f;  // also from -inf; not for NaN (-inf after -inf)
-      raised[n] = up ? v : mx[n];
-      grow |= up;
+    for (int r = 3; r < 15; r += 2) top = fmaxf(fmaxf(top, s[r]), s[r + 1]);
+    top = row_max(fmaxf(top, s[15]));
+    const bool up = (top - mx) * sc > 8.0f;  // also from -inf; not for NaN (-inf after -inf)
+    if (__ballot(up)) {
+      const float f = up ? __builtin_amdgcn_exp2f((mx - top) * sc) : 1.0f;
+      mx = up ? top : mx;
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < DV; ++i) o[i] *= f;
     }
-    if (__ballot(grow)) {
+    const float ref = (mx == kNegInf ? 0.0f : mx * sc) - MM::kLift;
+    V8 pt[2];
+    {
+      f32x16 e;
+      float part[2] = {0, 0};
 #pragma unroll
-      for (int n = 0; n < NM; ++n) {
-        const float m = raised[n];
-        const float f = mx[n] == m ? 1.0f : __builtin_amdgcn_exp2f((mx[n] - m) * sc);
-        mx[n] = m;
-        sum[n] *= f;
+      for (int r = 0; r < 16; ++r) {
+        e[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ref));
+        part[r & 1] += e[r];
+      }
+      sum += part[0] + part[1];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[n][i] *= f;
+      for (int w = 0; w < 2; ++w) {
+        f32x8 half;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) half[j] = e[8 * w + j];
+        pt[w] = __builtin_convertvector(half, V8);
       }
     }
-    V8 pt[NM];
+    // V^T: a column of the lane's, its eight tokens of a matrix step.
 #pragma unroll
-    for (int n = 0; n < NM; ++n) {
-      const float ref = (mx[n] == kNegInf ? 0.0f : mx[n] * sc) - MM::kLift;
-      f32x8 e;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = __builtin_amdgcn_exp2f(fmaf(s[n][j >> 2][j & 3], sc, -ref));
-        sum[n] += e[j];
-      }
-      pt[n] = __builtin_convertvector(e, V8);
-    }
-    // V^T: element i of the lane's columns, of its eight tokens.
-#pragma unroll
-    for (int hv = 0; hv < VH; ++hv)
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
         u32x4 lo, hi;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t w0 = x.v[2 * j][hv][e], w1 = x.v[2 * j + 1][hv][e];
+          const uint32_t w0 = v[8 * w + 2 * j][e], w1 = v[8 * w + 2 * j + 1][e];
           lo[j] = __builtin_amdgcn_perm(w1, w0, 0x05040100);
           hi[j] = __builtin_amdgcn_perm(w1, w0, 0x07060302);
         }
-#pragma unroll
-        for (int n = 0; n < NM; ++n) {
-          o[n][hv * DV + 2 * e] = MM::mul(__builtin_bit_cast(V8, lo), pt[n], o[n][hv * DV + 2 * e]);
-          o[n][hv * DV + 2 * e + 1] = MM::mul(__builtin_bit_cast(V8, hi), pt[n], o[n][hv * DV + 2 * e + 1]);
-        }
+        o[2 * e] = MM::mul(__builtin_bit_cast(V8, lo), pt[w], o[2 * e]);
+        o[2 * e + 1] = MM::mul(__builtin_bit_cast(V8, hi), pt[w], o[2 * e + 1]);
       }
-    if (slow) {
+    if (bad) {
       // The infinities and NaN left out above, token by token, added to the rows that see the token.
+#pragma unroll 1
       for (int t = 0; t < kTile; ++t) {
-        const int d = tok + t - it.cached;
-        const bool ok = t < 16 ? x.ok[0] : x.ok[1];
-        if (d < 0 || !ok || tok + t >= t1) continue;
-        const int64_t pg = page_of(tok + t);
-        const T* vp = vbase + pg * a.vc_page + ((tok + t) & in_page) * a.vc_token;
+        const int d = tok + t - it.q.cached;
+        if (d < 0 || d >= 64 || (t < 16 ? lost0 : lost1) || tok + t >= t1) continue;
+        const T* vp = reinterpret_cast<const T*>(vbase + page_of(tok + t) * (a.vc_page * 2) +
+                                                 static_cast<uint64_t>((tok + t) & in_page) * v_token);
+        float pr = 0;  // this row's probability of the token, from the lane that holds it
 #pragma unroll
-        for (int n = 0; n < NM; ++n) {
-          const bool seen = d < 64 && ((mask[n] >> (d & 63)) & 1);
-          float pr = 0;  // this row's probability of the token, from the lane that holds it
+        for (int j = 0; j < 16; ++j) {
+          const float x = __shfl(static_cast<float>(pt[j >> 3][j & 7]), ((t >> 2) & 1) * 32 + c);
+          if ((t >> 3) * 4 + (t & 3) == j) pr = x;
+        }
+        const bool seen = (mask >> d) & 1;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = __shfl(static_cast<float>(pt[n][j]), ((t & 15) >> 2) * 16 + c);
-            if (((t >> 4) * 4 + (t & 3)) == j) pr = v;
+        for (int i = 0; i < DV; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float x = static_cast<float>(vp[DV * (8 * (r >> 2) + 4 * h + (r & 3)) + i]);
+            if (seen && !(fabsf(x) < __builtin_inff())) o[i][r] += pr * x;
           }
-#pragma unroll
-          for (int hv = 0; hv < VH; ++hv)
-#pragma unroll
-            for (int i = 0; i < DV; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float v = static_cast<float>(vp[128 * hv + DV * (4 * g + r) + i]);
-                if (seen && !(fabsf(v) < __builtin_inff())) o[n][hv * DV + i][r] += pr * v;
-              }
-        }
-      }
-    }
-  };
-
-  // Tiles wk, wk + WK, ... of the chunk, loaded one ahead, their page numbers two ahead.
-  {
-    Tile x[2];
-    int tok = t0 + wk * kTile;
-    constexpr int kStep = WK * kTile;
-    auto next_pages = [&](int t, int (&pg)[2]) {
-      pg[0] = page_of(t);
-      pg[1] = page_of(t + 16);
-    };
-    if (tok < t1) {
-      int pg[2], pn[2];
-      next_pages(tok, pg);
-      next_pages(tok + kStep, pn);
-      load(x[0], tok, pg);
-      for (;;) {
-        if (tok + kStep < t1) {
-          load(x[1], tok + kStep, pn);
-          next_pages(tok + 2 * kStep, pn);
-        }
-        compute(x[0], tok);
-        tok += kStep;
-        if (tok >= t1) break;
-        if (tok + kStep < t1) {
-          load(x[0], tok + kStep, pn);
-          next_pages(tok + 2 * kStep, pn);
-        }
-        compute(x[1], tok);
-        tok += kStep;
-        if (tok >= t1) break;
       }
     }
   }
-#pragma unroll
-  for (int n = 0; n < NM; ++n) sum[n] = rows_sum(sum[n]);
+  sum = row_sum(sum);
 
   // Join the waves that shared rows, through LDS, and store: the output of a request in one part, or
   // this part's output, maximum and sum.
-  const bool whole = it.chunks == 1;
+  const bool whole = it.parts == 1;
   const int64_t slot = blockIdx.x;
   float* const part_o = p.part + slot * MB * D;
   float* const part_ml = p.part + static_cast<int64_t>(p.grid) * MB * D + slot * MB * 2;
-  typedef float FV __attribute__((ext_vector_type(DV)));
-  typedef FV FVM __attribute__((aligned(16)));  // in memory
-  auto store = [&](int m, int col, FV value) {  // `value`: DV columns from col of the block's row m
-    const int row = it.mb * MB + m;
-    if (row >= total) return;
-    if (whole) {
-      const int i = row / group, h = it.head * group + (row - i * group);
-      T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(it.start + i) * a.o_row + h * a.o_head + col;
-      typedef T TV __attribute__((ext_vector_type(DV)));
-      *reinterpret_cast<TV*>(dst) = __builtin_convertvector(value, TV);
-    } else {
-      *reinterpret_cast<FVM*>(part_o + m * D + col) = value;
-    }
+  constexpr int SV = DV < 4 ? DV : 4;  // columns stored at a time
+  typedef float FV __attribute__((ext_vector_type(SV)));
+  typedef T TV __attribute__((ext_vector_type(SV)));
+  // where row m of the block goes: the output, or the part
+  auto out_of = [&](int m) {
+    const int row = (it.mb << p.m_shift) + m, i = row / group;
+    return static_cast<T*>(a.out) + static_cast<int64_t>(it.q.start + i) * a.o_row +
+           (it.head * group + (row - i * group)) * a.o_head;
   };
   if constexpr (WK == 1) {
+    const int m = wm * 32 + c;
+    if ((it.mb << p.m_shift) + m >= total) return;
+    const float inv = whole ? (sum == 0 ? 0.0f : 1.0f / sum) : 1.0f;
+    T* const dst = whole ? out_of(m) : nullptr;
 #pragma unroll
-    for (int n = 0; n < NM; ++n) {
-      const int m = wm * 16 * NM + 16 * n + c;
-      const float inv = whole ? (sum[n] == 0 ? 0.0f : 1.0f / sum[n]) : 1.0f;
+    for (int r = 0; r < 16; ++r)
 #pragma unroll
-      for (int hv = 0; hv < VH; ++hv)
+      for (int i0 = 0; i0 < DV; i0 += SV) {
+        const int col = DV * (8 * (r >> 2) + 4 * h + (r & 3)) + i0;
+        FV x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          FV v;
-#pragma unroll
-          for (int i = 0; i < DV; ++i) v[i] = o[n][hv * DV + i][r] * inv;
-          store(m, 128 * hv + DV * (4 * g + r), v);
-        }
-      if (!whole && g == 0) {
-        part_ml[2 * m] = mx[n];
-        part_ml[2 * m + 1] = sum[n];
+        for (int i = 0; i < SV; ++i) x[i] = o[i0 + i][r] * inv;
+        if (whole) *reinterpret_cast<TV*>(dst + col) = __builtin_convertvector(x, TV);
+        else *reinterpret_cast<FV*>(part_o + m * D + col) = x;
       }
+    if (!whole && h == 0) {
+      part_ml[2 * m] = mx;
+      part_ml[2 * m + 1] = sum;
     }
   } else {
-    constexpr int MW = 16 * NM, LD = D + 4;  // rows of a wave; padded row
-    __shared__ __align__(16) float so[4][MW][LD];
-    __shared__ float sml[4][MW][2];
+    // over the stages, once every wave is through with them
+    float (*const so)[32][LD] = reinterpret_cast<float (*)[32][LD]>(lds);
+    float (*const sml)[32][2] = reinterpret_cast<float (*)[32][2]>(lds + WM * WK * 32 * LD * 4);
+    __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NM; ++n) {
+    for (int r = 0; r < 16; ++r)
 #pragma unroll
-      for (int hv = 0; hv < VH; ++hv)
+      for (int i0 = 0; i0 < DV; i0 += SV) {
+        FV x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          FV v;
-#pragma unroll
-          for (int i = 0; i < DV; ++i) v[i] = o[n][hv * DV + i][r];
-          *reinterpret_cast<FVM*>(&so[wave][16 * n + c][128 * hv + DV * (4 * g + r)]) = v;
-        }
-      if (g == 0) {
-        sml[wave][16 * n + c][0] = mx[n];
-        sml[wave][16 * n + c][1] = sum[n];
+        for (int i = 0; i < SV; ++i) x[i] = o[i0 + i][r];
+        *reinterpret_cast<FV*>(&so[wave][c][DV * (8 * (r >> 2) + 4 * h + (r & 3)) + i0]) = x;
       }
+    if (h == 0) {
+      sml[wave][c][0] = mx;
+      sml[wave][c][1] = sum;
     }
     __syncthreads();
-    constexpr int CH = D / DV;  // pieces of a row
-    for (int e = threadIdx.x; e < MB * CH; e += kAttnThreads) {
-      const int m = e / CH, col = (e % CH) * DV;
-      const int w0 = m / MW * WK, mw = m % MW;
+    constexpr int CH = D / SV;  // pieces of a row
+    const int rows = min(MB, total - (it.mb << p.m_shift));
+    for (int e = threadIdx.x; e < rows * CH; e += NT) {
+      const int m = e / CH, col = (e % CH) * SV;
+      const int w0 = m / 32 * WK, mw = m % 32;
       float top = kNegInf;
 #pragma unroll
       for (int w = 0; w < WK; ++w) top = fmaxf(top, sml[w0 + w][mw][0]);
-      FV v = {};
+      FV x = {};
       float l = 0;
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
         const float mw_max = sml[w0 + w][mw][0];
         const float f = mw_max == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((mw_max - top) * sc);
-        // A wave that saw nothing holds zeros only.
-        v += *reinterpret_cast<const FVM*>(&so[w0 + w][mw][col]) * f;
-        l += sml[w0 + w][mw][1] * f;
+        // A wave that saw nothing holds zeros (or NaN) only, and no maximum.
+        x += *reinterpret_cast<const FV*>(&so[w0 + w][mw][col]) * (mw_max == kNegInf ? 1.0f : f);
+        l += sml[w0 + w][mw][1] * (mw_max == kNegInf ? 1.0f : f);
       }
-      if (whole) v *= l == 0 ? 0.0f : 1.0f / l;
-      store(m, col, v);
-      if (!whole && col == 0 && it.mb * MB + m < total) {
+      if (whole) x *= l == 0 ? 0.0f : 1.0f / l;
+      if (whole) *reinterpret_cast<TV*>(out_of(m) + col) = __builtin_convertvector(x, TV);
+      else *reinterpret_cast<FV*>(part_o + m * D + col) = x;
+      if (!whole && col == 0) {
         part_ml[2 * m] = top;
         part_ml[2 * m + 1] = l;
       }
@@ -532,114 +555,137 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(verify_attention_arg
   }
 }
 
-// Joins the parts of a (row, head): one wave each, D / 64 values a lane. Rows of requests in one part are
+// Joins the parts of a (row, head), one wave each: lane i first takes part i's maximum and sum, then the
+// wave's halves take every other part's output, D / 32 values a lane. Rows of requests in one part are
 // stored already.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(verify_attention_args a, AttnLaunch p) {
-  constexpr int E = D / 64;
+__global__ void __launch_bounds__(256) attn_join_kernel(verify_attention_args a, AttnLaunch p) {
+  constexpr int E = D / 32;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int id = blockIdx.x * 4 + wave;
-  const int t = id / a.heads, h = id - t * a.heads;
+  const int t = id / a.heads, hq = id - t * a.heads;
   if (t >= a.n_rows) return;
-  // The row's request: the last one that starts at or before it and has rows there.
-  int b = -1;
+  int b = -1, start = 0, rows = 0;
   for (int b0 = 0; b0 < a.n_requests && b < 0; b0 += 64) {
     const int x = b0 + lane;
-    int s = 0, r = 0, c = 0, n = 0;
-    if (x < a.n_requests) attn_request(a, x, &s, &r, &c, &n);
-    const uint64_t hit = __ballot(t >= s && t < s + r);
-    if (hit) b = b0 + __ffsll(static_cast<unsigned long long>(hit)) - 1;
+    AttnRequest q{0, 0, 0, 0};
+    if (x < a.n_requests) q = attn_request(a, x);
+    const uint64_t hit = __ballot(t >= q.start && t < q.start + q.rows);
+    if (hit) {
+      const int from = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+      b = b0 + from;
+      start = __builtin_amdgcn_readlane(q.start, from);
+      rows = __builtin_amdgcn_readlane(q.rows, from);
+    }
   }
   if (b < 0) return;
-  AttnItem it;
-  if (!attn_find(a, p, lane, 0, b, &it) || it.chunks == 1) return;
-  const int group = a.heads / a.kv_heads;
-  const int kvh = h / group;
-  const int m_all = (t - it.start) * group + (h - kvh * group);
-  const int mb = m_all / p.m_block, m = m_all - mb * p.m_block;
-  const int mbs = (it.rows * group + p.m_block - 1) / p.m_block;
+  const int first = p.plan[2 * b], parts = p.plan[2 * b + 1];
+  if (parts == 1) return;
+  const int group = a.heads / a.kv_heads, kvh = hq / group;
+  const int m_all = (t - start) * group + (hq - kvh * group);
+  const int mb = m_all >> p.m_shift, m = m_all - (mb << p.m_shift);
+  const int mbs = (rows * group + (1 << p.m_shift) - 1) >> p.m_shift;
   const float sc = a.scale * 1.4426950408889634f;
-  const float* const ml = p.part + static_cast<int64_t>(p.grid) * p.m_block * D;
-  auto part = [&](int ch) {
-    return static_cast<int64_t>(it.first + attn_unit_block(p, ch * a.kv_heads + kvh, mb, mbs)) * p.m_block + m;
-  };
-  float top = kNegInf;
-  for (int ch = lane; ch < it.chunks; ch += 64) top = fmaxf(top, ml[2 * part(ch)]);
+  const float* const ml = p.part + (static_cast<int64_t>(p.grid) << p.m_shift) * D;
+  auto part = [&](int i) { return (attn_slot(p, first, i * a.kv_heads + kvh, mb, mbs) << p.m_shift) + m; };
+  const int h = lane >> 5, c = lane & 31;
+  typedef float FV __attribute__((ext_vector_type(E)));
+  FV o = {};
+  float l = 0, mx = kNegInf;
+  for (int i0 = 0; i0 < parts; i0 += 64) {
+    float pm = kNegInf, pl = 0;
+    if (i0 + lane < parts) {
+      const int64_t at = part(i0 + lane);
+      pm = ml[2 * at];
+      pl = ml[2 * at + 1];
+    }
+    const float top = fmaxf(mx, wave_max(pm));
+    const float ref = top == kNegInf ? 0.0f : top;
+    const float back = mx == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((mx - ref) * sc);  // what is there so far
+    // a part that saw nothing holds zeros (or NaN)
+    const float f = pm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((pm - ref) * sc);
+    mx = top;
+    l = l * back + wave_sum(pl * f);
+    o *= back;
+    const int n = min(64, parts - i0);
+    for (int i = 0; i < n; i += 8) {  // four parts a half wave, asked for at once
+      FV x[4];
+      float w[4];
 #pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-  float v[E] = {}, l = 0;
-#pragma unroll 4
-  for (int ch = 0; ch < it.chunks; ++ch) {
-    const int64_t at = part(ch);
-    const float mc = ml[2 * at], lc = ml[2 * at + 1];
-    const float f = mc == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((mc - top) * sc);
-    const float* src = p.part + at * D + E * lane;
+      for (int u = 0; u < 4; ++u) {
+        const int at = min(i + 2 * u + h, n - 1);
+        x[u] = *reinterpret_cast<const FV*>(p.part + part(i0 + at) * D + E * c);
+        w[u] = __shfl(f, at);
+      }
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += src[e] * f;
-    l += lc * f;
+      for (int u = 0; u < 4; ++u)
+        if (i + 2 * u + h < n) o += x[u] * w[u];
+    }
   }
-  const float inv = l == 0 ? 0.0f : 1.0f / l;
-  T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(t) * a.o_row + h * a.o_head + E * lane;
 #pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = static_cast<T>(v[e] * inv);
+  for (int e = 0; e < E; ++e) o[e] = row_sum(o[e]);
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  if (h) return;
+  T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(t) * a.o_row + hq * a.o_head + E * c;
+  typedef T TV __attribute__((ext_vector_type(E)));
+  TV x;
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = static_cast<T>(o[e] * inv);
+  *reinterpret_cast<TV*>(dst) = x;
 }
 
-// Launch shapes: rows a block holds, by the most query rows a (request, kv head) can have.
-struct AttnShape {
-  int nm, wk, m_block, per_cu;  // 16-row tiles a wave, waves along the tokens, rows a block, blocks a CU holds
-};
-
-inline AttnShape attn_shape(const verify_attention_args& a) {
-  const int m = a.max_rows * (a.heads / a.kv_heads);
-  if (m <= 16) return {1, 4, 16, a.dim == 256 ? 1 : 2};
-  if (m <= 32) return {2, 4, 32, 1};
-  if (a.dim == 256) return m <= 64 ? AttnShape{2, 2, 64, 1} : AttnShape{2, 1, 128, 1};
-  if (m <= 64) return {4, 4, 64, 1};
-  if (m <= 128) return {4, 2, 128, 1};
-  return {4, 1, 256, 1};
+// Waves along the rows of a block, by the most query rows a (request, kv head) can have. A block has 8
+// waves, as many as a CU holds at the kernel's registers; 4 with 256 values a head.
+inline int attn_wm(const verify_attention_args& a) {
+  const int m = a.max_rows * (a.heads / a.kv_heads), most = a.dim == 256 ? 4 : 8;
+  int wm = 1;
+  while (wm < most && 32 * wm < m) wm *= 2;
+  return wm;
 }
 
 // The grid and the workspace of a call; false if the blocks do not fit 31 bits.
 inline bool attn_plan(const verify_attention_args& a, AttnLaunch* p, int64_t* bytes) {
-  const AttnShape s = attn_shape(a);
-  const int m = a.max_rows * (a.heads / a.kv_heads);
-  const int64_t per_request = (m + s.m_block - 1) / s.m_block;
-  p->m_block = s.m_block;
-  p->target = 256 * s.per_cu;
+  const int m = a.max_rows * (a.heads / a.kv_heads), rows = 32 * attn_wm(a);
+  const int64_t per_request = (m + rows - 1) / rows;
+  p->m_shift = __builtin_ctz(rows);
+  p->least = kMinTiles * ((a.dim == 256 ? 4 : 8) / (rows / 32));
   p->swizzle = per_request > 1;
-  // sum over requests of row blocks x (heads x chunks, rounded): at most target for the chunks in all, one
-  // more chunk per row block and head, and the rounding.
-  const int64_t rowblocks = static_cast<int64_t>(a.n_requests) * per_request;
-  const int64_t grid = p->target + rowblocks * (a.kv_heads + (p->swizzle ? 7 : 0));
+  // Each (row block, head) rounds up to a whole number of parts, so the call makes up to `once` blocks more
+  // than the target. While that leaves room, all blocks fit the chip at once; with more, the target is
+  // several times what the chip holds, so that its last blocks leave little of it idle.
+  const int64_t row_blocks = static_cast<int64_t>(a.n_requests) * per_request, once = row_blocks * a.kv_heads;
+  p->target = static_cast<int32_t>(once <= kCus / 2 ? kCus - once : 4 * kCus);
+  const int64_t grid = p->target + once + (p->swizzle ? 7 * row_blocks : 0) + 8;
   if (grid > INT32_MAX) return false;
   p->grid = static_cast<int32_t>(grid);
   p->part = nullptr;
-  // A table that holds no more tokens than one chunk never splits.
-  const bool split = static_cast<int64_t>(a.width) * a.page_size > kMinChunk;
-  *bytes = split ? grid * s.m_block * (a.dim + 2) * 4 : 0;
+  p->plan = nullptr;
+  // A table that holds no more tokens than the least part never splits.
+  const bool split = static_cast<int64_t>(a.width) * a.page_size > p->least * kTile;
+  *bytes = split ? grid * rows * (a.dim + 2) * 4 + a.n_requests * 8 : 0;
   return true;
+}
+
+inline void attn_workspace(const verify_attention_args& a, AttnLaunch* p, void* workspace) {
+  p->part = static_cast<float*>(workspace);
+  p->plan = reinterpret_cast<int32_t*>(p->part + (static_cast<int64_t>(p->grid) << p->m_shift) * (a.dim + 2));
 }
 
 template <typename T, int D>
 hipError_t launch_attention_d(const verify_attention_args& a, const AttnLaunch& p, bool join, hipStream_t stream) {
-  const AttnShape s = attn_shape(a);
-  const dim3 grid(p.grid), block(kAttnThreads);
-  if (s.nm == 1) {
-    attn_kernel<T, D, 1, 4><<<grid, block, 0, stream>>>(a, p);
-  } else if (s.nm == 2 && s.wk == 4) {
-    attn_kernel<T, D, 2, 4><<<grid, block, 0, stream>>>(a, p);
-  } else if constexpr (D == 256) {
-    if (s.wk == 2) attn_kernel<T, D, 2, 2><<<grid, block, 0, stream>>>(a, p);
-    else attn_kernel<T, D, 2, 1><<<grid, block, 0, stream>>>(a, p);
-  } else {
-    if (s.wk == 4) attn_kernel<T, D, 4, 4><<<grid, block, 0, stream>>>(a, p);
-    else if (s.wk == 2) attn_kernel<T, D, 4, 2><<<grid, block, 0, stream>>>(a, p);
-    else attn_kernel<T, D, 4, 1><<<grid, block, 0, stream>>>(a, p);
+  constexpr int W = D == 256 ? 4 : 8;
+  const dim3 grid(p.grid), block(64 * W);
+  switch (attn_wm(a)) {
+    case 1: attn_kernel<T, D, 1, W><<<grid, block, 0, stream>>>(a, p); break;
+    case 2: attn_kernel<T, D, 2, W / 2><<<grid, block, 0, stream>>>(a, p); break;
+    case 4: attn_kernel<T, D, 4, W / 4><<<grid, block, 0, stream>>>(a, p); break;
+    default:
+      if constexpr (D != 256) attn_kernel<T, D, 8, 1><<<grid, block, 0, stream>>>(a, p);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !join) return e;
   const int64_t waves = static_cast<int64_t>(a.n_rows) * a.heads;
-  attn_join_kernel<T, D><<<dim3(static_cast<unsigned>((waves + 3) / 4)), block, 0, stream>>>(a, p);
+  attn_join_kernel<T, D><<<dim3(static_cast<unsigned>((waves + 3) / 4)), dim3(256), 0, stream>>>(a, p);
   return hipGetLastError();
 }
 

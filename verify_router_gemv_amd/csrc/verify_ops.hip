@@ -49,7 +49,7 @@ extern "C" moe_status verify_tree_attention(const verify_attention_args* a, void
   int64_t bytes = 0;
   if (!attn_plan(*a, &p, &bytes)) return MOE_ERR_UNSUPPORTED;
   if (!workspace_ok(workspace, workspace_bytes, bytes)) return MOE_ERR_INVALID_ARG;
-  p.part = static_cast<float*>(workspace);
+  if (bytes) attn_workspace(*a, &p, workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return hip_status(a->type == VERIFY_BF16 ? launch_attention<__bf16>(*a, p, bytes != 0, s)
                                            : launch_attention<_Float16>(*a, p, bytes != 0, s));
