@@ -186,13 +186,18 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Which of the four tokens at `at` .. `at` + 3 a row sees, as bits: all before `cached`, drafted ones by the
-// row's mask, none from `end` on.
+// row's mask, none from `end` on. (Arithmetic, no branches, as in all of the edge's work below: with lanes
+// taking different ways there, the wide heads' kernel, which keeps part of its registers in accumulation
+// registers, came out with wrong values in the lanes that had been away.)
 __device__ __forceinline__ uint32_t attn_seen(int at, int cached, int end, uint64_t mask) {
   const int d = at - cached;
-  const uint32_t past = static_cast<uint32_t>(mask << min(max(-d, 0), 3)) | ((1u << min(max(-d, 0), 4)) - 1u);
-  const uint32_t bits = d < 0 ? past : d < 64 ? static_cast<uint32_t>(mask >> (d & 63)) : 0u;
+  const int before = min(max(-d, 0), 4);
+  const uint32_t past = static_cast<uint32_t>(mask >> min(max(d, 0), 63)) & static_cast<uint32_t>((d - 64) >> 31);
+  const uint32_t bits = (past << before) | ((1u << before) - 1u);
   return bits & ((1u << min(max(end - at, 0), 4)) - 1u);
 }
+// All bits of a word where x < y.
+__device__ __forceinline__ uint32_t less_mask(int x, int y) { return static_cast<uint32_t>((x - y) >> 31); }
 
 template <typename T, int D, int WM, int WK>
 __global__ void __launch_bounds__(64 * WM * WK, D == 256 ? 1 : 2)
@@ -230,8 +235,9 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
   // unseen (page 0 is read instead, and dropped).
   auto page_of = [&](int tok) {
     const int col = tok >> shift;
-    const int page = tok < t1 && col < a.width ? pages[col] : -1;
-    return page < a.n_pages ? page : -1;
+    const bool in = tok < t1 && col < a.width;
+    const int page = pages[in ? col : 0];
+    return in && page < a.n_pages ? page : -1;
   };
 
   // A stage: 32 tokens' keys, then their values, 2 D bytes a token. One load of a wave writes 1 KB of it,
@@ -277,7 +283,9 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
       const char* const src = is_k ? kbase + pg * (a.kc_page * 2) + static_cast<uint64_t>(at) * k_token
                                    : vbase + pg * (a.vc_page * 2) + static_cast<uint64_t>(at) * v_token;
       const uint32_t off = is_k ? k_lane + 16 * (k_piece ^ twist(row)) : v_lane;
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+      // (The wait states: a vector instruction may just have written the address's scalars, and the
+      // compiler does not see that this text reads them.)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                    :: "s"(to + n * 1024), "v"(off), "s"(src) : "memory");
     }
     lost |= ((page0 < 0 ? 1u : 0u) | (page1 < 0 ? 2u : 0u)) << (2 * (NS > 1 ? NS - 1 : 0));
@@ -315,14 +323,37 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
   const int k_row = c * RB, k_twist = h ^ twist(c);
   const int v_row = kTile * RB + 4 * h * RB + 2 * DV * c;
 
+  auto load_keys = [&](const char* at, u32x4 (&k)[KK]) {
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) k[kk] = *reinterpret_cast<const u32x4*>(at + k_row + 16 * (2 * kk ^ k_twist));
+  };
+  auto scores = [&](const u32x4 (&k)[KK]) {
+    f32x16 s = {};
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) s = MM::mul(__builtin_bit_cast(V8, k[kk]), q[kk], s);
+    return s;
+  };
+  // With four stages the rows are many and the matrix cores count: a tile is scored in the round before
+  // its own, between the exponentials of the tile before it, which the matrix cores would else wait for.
+  constexpr bool kAhead = NS == 4;
+  constexpr int kWait = kAhead ? NS - 3 : NS - 2;  // tiles that may still be under way when a round begins
+  f32x16 s;
+  if constexpr (kAhead) {
+    if (mine > 2) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(2 * NI) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+    u32x4 k[KK];
+    load_keys(stream, k);
+    s = scores(k);
+  }
   for (int tile = 0; tile < rounds; ++tile) {
     const int tok = tok_of(tile);
     if constexpr (NS == 1) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     } else {
-      // The tile has arrived when at most the loads of the NS - 2 tiles after it are still under way; every
-      // wave has also finished with the stage that is asked for next.
-      if (tile + NS - 2 < mine) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"((NS - 2) * NI) : "memory");
+      // The tile (scored ahead: the one after it) has arrived when at most the loads of the tiles after it are
+      // still under way; every wave has also finished with the stage that is asked for next.
+      if (tile + NS - 2 < mine) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(kWait * NI) : "memory");
       else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       asm volatile("s_barrier" ::: "memory");
       if (tile + NS - 1 < mine) ask(tile + NS - 1);
@@ -333,9 +364,8 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
     }
     const char* const at0 = stream + (NS > 1 ? tile % NS * kStage : 0);
     u32x4 k[KK];
+    if constexpr (!kAhead) load_keys(at0, k);
     uint32_t v[16][VW];
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) k[kk] = *reinterpret_cast<const u32x4*>(at0 + k_row + 16 * (2 * kk ^ k_twist));
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const char* const src = at0 + v_row + (8 * (j >> 2) + (j & 3)) * RB;
@@ -356,12 +386,10 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (tile + 1 < mine) ask(tile + 1);
     }
-    f32x16 s = {};
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) s = MM::mul(__builtin_bit_cast(V8, k[kk]), q[kk], s);
+    if constexpr (!kAhead) s = scores(k);
 
     const bool edge = tok + kTile > it.q.cached || lost0 || lost1;  // some token may be unseen
-    uint32_t bad = 0;
+    bool bad = false;
     if (edge) {
       // Scores of unseen tokens are replaced, whatever they are; values of tokens that nobody may see
       // (past the end, on no page) are zeroed, and a drafted token's infinity or NaN is found, which the
@@ -369,30 +397,37 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int at = tok + 8 * j + 4 * h;
-        const int end = (j < 2 ? lost0 : lost1) ? at : t1;
-        const uint32_t bits = attn_seen(at, it.q.cached, end, mask);
+        const uint32_t bits = attn_seen(at, it.q.cached, (j < 2 ? lost0 : lost1) ? at : t1, mask);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          s[4 * j + r] = (bits >> r) & 1 ? s[4 * j + r] : kNegInf;
-          const bool real = at + r < end, drafted = at + r >= it.q.cached;
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const uint32_t w = real ? v[4 * j + r][e] : 0;
-            v[4 * j + r][e] = w;
-            bad |= drafted ? (w & MM::kExp) + MM::kExpStep : 0;
-          }
+          const uint32_t keep = -((bits >> r) & 1);
+          const float x = s[4 * j + r];
+          s[4 * j + r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & keep) | (0xff800000u & ~keep));
         }
       }
-      bad = __ballot((bad & 0x80008000u) != 0) != 0;
-      if (bad) {  // keep them out of the product
+      if (tok + kTile > t1 || lost0 || lost1) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t real = less_mask(tok + 8 * (j >> 2) + 4 * h + (j & 3), (j < 8 ? lost0 : lost1) ? 0 : t1);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) v[j][e] &= real;
+        }
+      }
+      uint32_t found = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) found |= (v[j][e] & MM::kExp) + MM::kExpStep;
+      bad = __ballot((found & 0x80008000u) != 0) != 0;
+      if (bad) {  // keep the drafted tokens' out of the product
 #pragma unroll
         for (int j = 0; j < 16; ++j)
 #pragma unroll
           for (int e = 0; e < VW; ++e) {
             const uint32_t w = v[j][e];
             const uint32_t x = (w & MM::kExp) + MM::kExpStep;
-            const bool drafted = tok + 8 * (j >> 2) + 4 * h + (j & 3) >= it.q.cached;
-            if (drafted) v[j][e] = (x & 0x8000u ? 0 : w & 0xffffu) | (x & 0x80000000u ? 0 : w & 0xffff0000u);
+            const uint32_t wrong = ((x >> 15) & 0x00010001u) * 0xffffu;  // the halves that are no number
+            v[j][e] = w & ~(wrong & ~less_mask(tok + 8 * (j >> 2) + 4 * h + (j & 3), it.q.cached));
           }
       }
     }
@@ -430,6 +465,11 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
         pt[w] = __builtin_convertvector(half, V8);
       }
     }
+    if constexpr (kAhead) {  // (past the wave's last tile: of whatever the stage holds, for nothing)
+      u32x4 k[KK];
+      load_keys(stream + (tile + 1) % NS * kStage, k);
+      s = scores(k);
+    }
     // V^T: a column of the lane's, its eight tokens of a matrix step.
 #pragma unroll
     for (int w = 0; w < 2; ++w)
@@ -465,7 +505,8 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const float x = static_cast<float>(vp[DV * (8 * (r >> 2) + 4 * h + (r & 3)) + i]);
-            if (seen && !(fabsf(x) < __builtin_inff())) o[i][r] += pr * x;
+            const uint32_t add = -static_cast<uint32_t>(seen & !(fabsf(x) < __builtin_inff()));
+            o[i][r] += __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, pr * x) & add);
           }
       }
     }
