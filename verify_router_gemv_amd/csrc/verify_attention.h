@@ -254,8 +254,28 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
       (__attribute__((address_space(3))) char*)stream));
   auto twist = [](int token) { return (D == 64 ? token >> 1 : token) & (CR < 16 ? CR - 1 : 15); };
   const int lr = lane / CR, lc = lane % CR;           // a load's token and piece of this lane
-  const uint32_t k_lane = lr * k_token, v_lane = lr * v_token + 16 * lc;
-  const int k_piece = lc ^ twist(lr);
+  // The wave's j-th load: the j WM + wm-th of a tile, whose first token is row `row` of keys or values.
+  struct Part {
+    bool is_k;
+    int n, row;
+  };
+  auto part_of = [&](int j) {
+    const int n = j * WM + wm;
+    return Part{n < KI, n, (n < KI ? n : n - KI) * (512 / D)};
+  };
+  auto offset_of = [&](int j) {  // of this lane's piece from the half tile's first token
+    const Part l = part_of(j);
+    const uint32_t token = (l.row & 15) + lr;
+    return l.is_k ? token * k_token + 16 * (lc ^ twist(token)) : token * v_token + 16 * lc;
+  };
+  constexpr bool kKeep = WM == 2;  // the offsets stay in registers; with other shares only ...
+  uint32_t offset[kKeep ? NI : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) offset[j] = offset_of(j);
+  }
+  // ... the first ones, and what a load lies further on is added.
+  const uint32_t k_near = lr * k_token, v_near = lr * v_token + 16 * lc;
   auto tok_of = [&](int tile) { return t0 + (tile * WK + wk) * kTile; };
   // Lane i: the page of half i % 2 of the tile i / 2 after the last multiple of 32 (looked up 32 tiles at a
   // time, so that the loop waits for nothing but its tiles).
@@ -272,21 +292,30 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
     const int page1 = __builtin_amdgcn_readlane(page_list, 2 * (tile & 31) + 1);
     const int pg0 = max(page0, 0), pg1 = max(page1, 0);
     const uint32_t to = lds0 + (NS > 1 ? tile % NS * kStage : 0);
-    const int place = tok & in_page, place1 = (tok + 16) & in_page;
+    const uint64_t place0 = tok & in_page, place1 = (tok + 16) & in_page;
+    const char* const k0 = kbase + pg0 * (a.kc_page * 2) + place0 * k_token;
+    const char* const k1 = kbase + pg1 * (a.kc_page * 2) + place1 * k_token;
+    const char* const v0 = vbase + pg0 * (a.vc_page * 2) + place0 * v_token;
+    const char* const v1 = vbase + pg1 * (a.vc_page * 2) + place1 * v_token;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int n = j * WM + wm;
-      const bool is_k = n < KI;
-      const int row = (is_k ? n : n - KI) * (512 / D);
-      const int64_t pg = row < 16 ? pg0 : pg1;
-      const uint32_t at = (row < 16 ? place : place1) + (row & 15);
-      const char* const src = is_k ? kbase + pg * (a.kc_page * 2) + static_cast<uint64_t>(at) * k_token
-                                   : vbase + pg * (a.vc_page * 2) + static_cast<uint64_t>(at) * v_token;
-      const uint32_t off = is_k ? k_lane + 16 * (k_piece ^ twist(row)) : v_lane;
+      const Part l = part_of(j);
+      const char* src;
+      uint32_t off;
+      if constexpr (WM >= 4) {  // two or four loads: each works out its own token's address
+        const int64_t pg = l.row < 16 ? pg0 : pg1;
+        const uint64_t at = (l.row < 16 ? place0 : place1) + (l.row & 15);
+        src = l.is_k ? kbase + pg * (a.kc_page * 2) + at * k_token : vbase + pg * (a.vc_page * 2) + at * v_token;
+        off = l.is_k ? k_near + 16 * (lc ^ twist(lr) ^ twist(l.row)) : v_near;
+      } else {
+        src = l.is_k ? (l.row < 16 ? k0 : k1) : l.row < 16 ? v0 : v1;
+      }
+      if constexpr (kKeep) off = offset[j];
+      else if constexpr (WM < 4) off = l.is_k ? k_near + (l.row & 15) * k_token + 16 * (lc ^ twist(lr) ^ twist(l.row)) : v_near + (l.row & 15) * v_token;
       // (The wait states: a vector instruction may just have written the address's scalars, and the
       // compiler does not see that this text reads them.)
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-                   :: "s"(to + n * 1024), "v"(off), "s"(src) : "memory");
+                   :: "s"(to + l.n * 1024), "v"(off), "s"(src) : "memory");
     }
     lost |= ((page0 < 0 ? 1u : 0u) | (page1 < 0 ? 2u : 0u)) << (2 * (NS > 1 ? NS - 1 : 0));
   };
