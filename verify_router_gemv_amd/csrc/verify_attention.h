@@ -268,7 +268,7 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
     const uint32_t token = (l.row & 15) + lr;
     return l.is_k ? token * k_token + 16 * (lc ^ twist(token)) : token * v_token + 16 * lc;
   };
-  constexpr bool kKeep = WM == 2;  // the offsets stay in registers; with other shares only ...
+  constexpr bool kKeep = WM > 1;  // the offsets stay in registers; of a wave that has all 2 KI loads only ...
   uint32_t offset[kKeep ? NI : 1];
   if constexpr (kKeep) {
 #pragma unroll
@@ -277,47 +277,53 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
   // ... the first ones, and what a load lies further on is added.
   const uint32_t k_near = lr * k_token, v_near = lr * v_token + 16 * lc;
   auto tok_of = [&](int tile) { return t0 + (tile * WK + wk) * kTile; };
-  // Lane i: the page of half i % 2 of the tile i / 2 after the last multiple of 32 (looked up 32 tiles at a
-  // time, so that the loop waits for nothing but its tiles).
-  int page_list = 0;
+  // Lane i: where the keys and values of half i % 2 of the tile i / 2 after the last multiple of 32 begin. The
+  // lanes work this out for 32 tiles at a time, so that the loop waits for nothing but its tiles and has
+  // no address arithmetic; halves without a page are marked.
+  uint32_t k_lo = 0, k_hi = 0, v_lo = 0, v_hi = 0;
+  uint64_t no_page = 0;
   auto look_up = [&](int tile) {
-    page_list = page_of(tok_of(tile + (lane >> 1)) + 16 * (lane & 1));
+    const int half = tok_of(tile + (lane >> 1)) + 16 * (lane & 1);
+    const int page = page_of(half);
+    const int64_t pg = max(page, 0);
+    const uint64_t place = half & in_page;
+    const uint64_t ka = reinterpret_cast<uint64_t>(kbase) + pg * (a.kc_page * 2) + place * k_token;
+    const uint64_t va = reinterpret_cast<uint64_t>(vbase) + pg * (a.vc_page * 2) + place * v_token;
+    k_lo = static_cast<uint32_t>(ka), k_hi = static_cast<uint32_t>(ka >> 32);
+    v_lo = static_cast<uint32_t>(va), v_hi = static_cast<uint32_t>(va >> 32);
+    no_page = __ballot(page < 0);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  };
+  auto read_base = [](uint32_t lo, uint32_t hi, int i) {
+    return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, i))) << 32 |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, i));
   };
   uint32_t lost = 0;          // two bits a tile in flight, the one in use lowest: its halves without a page
   auto ask = [&](int tile) {  // the wave's loads of a tile
-    const int tok = tok_of(tile);
     if ((tile & 31) == 0) look_up(tile);
-    const int page0 = __builtin_amdgcn_readlane(page_list, 2 * (tile & 31));
-    const int page1 = __builtin_amdgcn_readlane(page_list, 2 * (tile & 31) + 1);
-    const int pg0 = max(page0, 0), pg1 = max(page1, 0);
+    const int i = 2 * (tile & 31);
     const uint32_t to = lds0 + (NS > 1 ? tile % NS * kStage : 0);
-    const uint64_t place0 = tok & in_page, place1 = (tok + 16) & in_page;
-    const char* const k0 = kbase + pg0 * (a.kc_page * 2) + place0 * k_token;
-    const char* const k1 = kbase + pg1 * (a.kc_page * 2) + place1 * k_token;
-    const char* const v0 = vbase + pg0 * (a.vc_page * 2) + place0 * v_token;
-    const char* const v1 = vbase + pg1 * (a.vc_page * 2) + place1 * v_token;
+    uint64_t k0, k1, v0, v1;
+    if constexpr (WM < 4) {
+      k0 = read_base(k_lo, k_hi, i), k1 = read_base(k_lo, k_hi, i + 1);
+      v0 = read_base(v_lo, v_hi, i), v1 = read_base(v_lo, v_hi, i + 1);
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const Part l = part_of(j);
-      const char* src;
+      uint64_t src;
+      if constexpr (WM < 4) src = l.is_k ? (l.row < 16 ? k0 : k1) : l.row < 16 ? v0 : v1;
+      else if constexpr (KI % WM == 0) src = j < NI / 2 ? read_base(k_lo, k_hi, i + (l.row >> 4)) : read_base(v_lo, v_hi, i + (l.row >> 4));
+      else src = l.is_k ? read_base(k_lo, k_hi, i + (l.row >> 4)) : read_base(v_lo, v_hi, i + (l.row >> 4));
       uint32_t off;
-      if constexpr (WM >= 4) {  // two or four loads: each works out its own token's address
-        const int64_t pg = l.row < 16 ? pg0 : pg1;
-        const uint64_t at = (l.row < 16 ? place0 : place1) + (l.row & 15);
-        src = l.is_k ? kbase + pg * (a.kc_page * 2) + at * k_token : vbase + pg * (a.vc_page * 2) + at * v_token;
-        off = l.is_k ? k_near + 16 * (lc ^ twist(lr) ^ twist(l.row)) : v_near;
-      } else {
-        src = l.is_k ? (l.row < 16 ? k0 : k1) : l.row < 16 ? v0 : v1;
-      }
       if constexpr (kKeep) off = offset[j];
-      else if constexpr (WM < 4) off = l.is_k ? k_near + (l.row & 15) * k_token + 16 * (lc ^ twist(lr) ^ twist(l.row)) : v_near + (l.row & 15) * v_token;
-      // (The wait states: a vector instruction may just have written the address's scalars, and the
-      // compiler does not see that this text reads them.)
+      else off = l.is_k ? k_near + (l.row & 15) * k_token + 16 * (lc ^ twist(lr) ^ twist(l.row)) : v_near + (l.row & 15) * v_token;
+      // (The wait states: a vector instruction has just written the address's scalars, and the compiler
+      // does not see that this text reads them.)
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                    :: "s"(to + l.n * 1024), "v"(off), "s"(src) : "memory");
     }
-    lost |= ((page0 < 0 ? 1u : 0u) | (page1 < 0 ? 2u : 0u)) << (2 * (NS > 1 ? NS - 1 : 0));
+    lost |= (static_cast<uint32_t>(no_page >> i) & 3u) << (2 * (NS > 1 ? NS - 1 : 0));
   };
 
   // Tiles of the stream with the most of them: all waves of the block go round as often.
@@ -418,6 +424,8 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
     if constexpr (!kAhead) s = scores(k);
 
     const bool edge = tok + kTile > it.q.cached || lost0 || lost1;  // some token may be unseen
+    int first = tok + 4 * h;  // the lane's first token; opaque, or its sixteen tokens' numbers would be
+    asm("" : "+v"(first));    // kept in registers through the loop
     bool bad = false;
     if (edge) {
       // Scores of unseen tokens are replaced, whatever they are; values of tokens that nobody may see
@@ -425,7 +433,7 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
       // matrix product would spread to the rows that do not see the token.
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int at = tok + 8 * j + 4 * h;
+        const int at = first + 8 * j;
         const uint32_t bits = attn_seen(at, it.q.cached, (j < 2 ? lost0 : lost1) ? at : t1, mask);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -437,7 +445,7 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
       if (tok + kTile > t1 || lost0 || lost1) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const uint32_t real = less_mask(tok + 8 * (j >> 2) + 4 * h + (j & 3), (j < 8 ? lost0 : lost1) ? 0 : t1);
+          const uint32_t real = less_mask(first + 8 * (j >> 2) + (j & 3), (j < 8 ? lost0 : lost1) ? 0 : t1);
 #pragma unroll
           for (int e = 0; e < VW; ++e) v[j][e] &= real;
         }
@@ -456,7 +464,7 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
             const uint32_t w = v[j][e];
             const uint32_t x = (w & MM::kExp) + MM::kExpStep;
             const uint32_t wrong = ((x >> 15) & 0x00010001u) * 0xffffu;  // the halves that are no number
-            v[j][e] = w & ~(wrong & ~less_mask(tok + 8 * (j >> 2) + 4 * h + (j & 3), it.q.cached));
+            v[j][e] = w & ~(wrong & ~less_mask(first + 8 * (j >> 2) + (j & 3), it.q.cached));
           }
       }
     }
