@@ -16,20 +16,9 @@ namespace verify {
 
 constexpr int kRopeThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ f32x8 load8(const T* p);
-template <>
-__device__ __forceinline__ f32x8 load8<float>(const float* p) {
+__device__ __forceinline__ f32x8 load8(const float* p) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
-template <>
-__device__ __forceinline__ f32x8 load8<__bf16>(const __bf16* p) {
-  return __builtin_convertvector(*reinterpret_cast<const bf16x8*>(p), f32x8);
-}
-template <>
-__device__ __forceinline__ f32x8 load8<_Float16>(const _Float16* p) {
-  return __builtin_convertvector(*reinterpret_cast<const f16x8*>(p), f32x8);
 }
 __device__ __forceinline__ void store8(__bf16* p, f32x8 v) {
   *reinterpret_cast<bf16x8*>(p) = __builtin_convertvector(v, bf16x8);
@@ -38,16 +27,32 @@ __device__ __forceinline__ void store8(_Float16* p, f32x8 v) {
   *reinterpret_cast<f16x8*>(p) = __builtin_convertvector(v, f16x8);
 }
 
+template <typename T>
+struct Raw8 {  // eight values as they lie in memory
+  typedef T V __attribute__((ext_vector_type(8)));
+  V v;
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+      v = V{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    } else {
+      v = *reinterpret_cast<const V*>(p);
+    }
+  }
+  __device__ __forceinline__ f32x8 get() const { return __builtin_convertvector(v, f32x8); }
+};
+
 template <typename TI, typename TC, int D>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(verify_rope_args a) {
   constexpr int L = D / 8;                 // lanes per head
   constexpr int HB = kRopeThreads / L;     // heads per step of the block
+  constexpr int U = 3;                     // steps whose heads are asked for at once
   __shared__ float2 turn[D / 2];
   const int t = blockIdx.x, l = threadIdx.x % L;
   const int items = a.heads + 2 * a.kv_heads;
   const int slot = a.slots[t];
-  const int page = slot / a.page_size, place = slot - page * a.page_size;
-  if (slot < 0 || page >= a.n_pages) return;  // the whole block
+  const int position = a.positions[t];
+  const int half = a.n_freq;
 
   auto source = [&](int item) -> const TI* {
     if (item < a.heads) return static_cast<const TI*>(a.q) + t * a.q_row + item * a.q_head;
@@ -55,76 +60,81 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(verify_rope_args a) 
     if (item < a.kv_heads) return static_cast<const TI*>(a.k) + t * a.k_row + item * a.k_head;
     return static_cast<const TI*>(a.v) + t * a.v_row + (item - a.kv_heads) * a.v_head;
   };
-  int item = blockIdx.y * HB + threadIdx.x / L;
-  f32x8 x{};
-  if (item < items) x = load8<TI>(source(item) + 8 * l);
-
-  const int half = a.n_freq;
+  const int mine = threadIdx.x / L;
+  Raw8<TI> x[U];
+  auto ask = [&](int step) {  // a thread past the last head takes the last one again, and stores nothing
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int item = (step + u * static_cast<int>(gridDim.y)) * HB + mine;
+      x[u].load(source(item < items ? item : items - 1) + 8 * l);
+    }
+  };
+  int step = blockIdx.y;
+  ask(step);
+  f32x8 wq{}, wk{};
+  if (a.q_weight) wq = load8(a.q_weight + 8 * l);
+  if (a.k_weight) wk = load8(a.k_weight + 8 * l);
   if (static_cast<int>(threadIdx.x) < half) {
-    const double angle = static_cast<double>(a.positions[t]) * static_cast<double>(a.inv_freq[threadIdx.x]);
+    const double angle = static_cast<double>(position) * static_cast<double>(a.inv_freq[threadIdx.x]);
     const double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
     float s, c;
     sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
     turn[threadIdx.x] = make_float2(c, s);
   }
+  const int page = slot / a.page_size, place = slot - page * a.page_size;
+  if (slot < 0 || page >= a.n_pages) return;  // the whole block
   __syncthreads();
+  TC* const ko = static_cast<TC*>(a.k_cache) + page * a.kc_page + place * a.kc_token;
+  TC* const vo = static_cast<TC*>(a.v_cache) + page * a.vc_page + place * a.vc_token;
 
   for (;;) {
-    const int next = item + gridDim.y * HB;
-    f32x8 xn{};
-    if (next < items) xn = load8<TI>(source(next) + 8 * l);
-    const bool is_q = item < a.heads, is_v = item >= a.heads + a.kv_heads;
-    // Lanes of a head past the last take part in the shuffles (with zeros) and store nothing.
-    const float* w = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
-    f32x8 y = x;
-    float ss = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
+    for (int u = 0; u < U; ++u) {
+      const int at = (step + u * static_cast<int>(gridDim.y)) * HB;
+      if (at >= items) break;  // uniform over the block
+      const int item = at + mine;
+      const bool is_q = item < a.heads, is_v = item >= a.heads + a.kv_heads;
+      f32x8 y = x[u].get();
+      if (item < items && is_v) store8(vo + (item - a.heads - a.kv_heads) * a.vc_head + 8 * l, y);
+      float ss = 0;
 #pragma unroll
-    for (int s = 1; s < L; s <<= 1) ss += __shfl_xor(ss, s);
-    if (w) {
-      const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-      y = x * r * load8<float>(w + 8 * l);
-    }
-    f32x8 z = y;
-    if (a.interleaved) {
-      if (8 * l < 2 * half) {
+      for (int j = 0; j < 8; ++j) ss += y[j] * y[j];
+      ss = moe::group_sum<L>(ss);
+      if (is_q ? a.q_weight : a.k_weight) y *= (is_q ? wq : wk) * (1.0f / sqrtf(ss * (1.0f / D) + a.eps));
+      f32x8 z = y;
+      if (a.interleaved) {
+        if (8 * l < 2 * half) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float2 cs = turn[4 * l + j / 2];
-          z[j] = y[j] * cs.x - y[j + 1] * cs.y;
-          z[j + 1] = y[j + 1] * cs.x + y[j] * cs.y;
+          for (int j = 0; j < 8; j += 2) {
+            const float2 cs = turn[4 * l + j / 2];
+            z[j] = y[j] * cs.x - y[j + 1] * cs.y;
+            z[j + 1] = y[j + 1] * cs.x + y[j] * cs.y;
+          }
         }
-      }
-    } else {
-      const int hop = half / 8;  // lanes to the other half of the pair
-      const bool low = l < hop, in = l < 2 * hop;
-      const int lane = threadIdx.x & 63;
-      const int from = in ? (low ? lane + hop : lane - hop) : lane;
-      f32x8 o;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = __shfl(y[j], from);
-      if (in) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 cs = turn[8 * (low ? l : l - hop) + j];
-          z[j] = y[j] * cs.x + (low ? -o[j] : o[j]) * cs.y;
-        }
-      }
-    }
-    if (item < items) {
-      if (is_q) {
-        store8(static_cast<TC*>(a.q_out) + t * a.o_row + item * a.o_head + 8 * l, z);
-      } else if (!is_v) {
-        store8(static_cast<TC*>(a.k_cache) + page * a.kc_page + (item - a.heads) * a.kc_head + place * a.kc_token + 8 * l, z);
       } else {
-        store8(static_cast<TC*>(a.v_cache) + page * a.vc_page + (item - a.heads - a.kv_heads) * a.vc_head +
-                   place * a.vc_token + 8 * l, x);
+        const int hop = half / 8;  // lanes to the other half of the pair
+        const bool low = l < hop, in = l < 2 * hop;
+        const int lane = threadIdx.x & 63;
+        const int from = in ? (low ? lane + hop : lane - hop) : lane;
+        f32x8 o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __shfl(y[j], from);
+        if (in) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 cs = turn[8 * (low ? l : l - hop) + j];
+            z[j] = y[j] * cs.x + (low ? -o[j] : o[j]) * cs.y;
+          }
+        }
+      }
+      if (item < items && !is_v) {
+        if (is_q) store8(static_cast<TC*>(a.q_out) + t * a.o_row + item * a.o_head + 8 * l, z);
+        else store8(ko + (item - a.heads) * a.kc_head + 8 * l, z);
       }
     }
-    if (next - static_cast<int>(threadIdx.x / L) >= items) break;  // uniform over the block
-    item = next;
-    x = xn;
+    step += U * gridDim.y;
+    if (step * HB >= items) break;
+    ask(step);
   }
 }
 
