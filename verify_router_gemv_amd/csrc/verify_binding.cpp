@@ -141,6 +141,17 @@ struct On {
   }
 };
 
+// A contiguous piece of a contiguous tensor, of the same type (what narrow and view give, without their
+// dispatch: the small tensors of one call share one allocation).
+at::Tensor piece(const at::Tensor& of, int64_t from, at::IntArrayRef sizes) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(of.storage()), of.key_set(),
+                                                          of.dtype());
+  c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(of.storage_offset() + from);
+  impl->set_sizes_contiguous(sizes);
+  return t;
+}
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 // A new reference to `o`, or the tensor made in its place.
 PyObject* given(PyObject* o, const at::Tensor& made) {
@@ -195,10 +206,10 @@ PyObject* round_slots(PyObject*, PyObject* const* o, Py_ssize_t n) {
     at::Tensor made[5];
     if (o[8] == Py_None) {
       const at::Tensor buf = c.empty({B + 3 + 2 * N}, at::kInt);
-      made[1] = buf.narrow(0, 0, N);
-      made[2] = buf.narrow(0, N, N);
-      made[0] = buf.narrow(0, 2 * N, B + 1);
-      made[4] = buf.narrow(0, 2 * N + B + 1, 2);
+      made[1] = piece(buf, 0, {N});
+      made[2] = piece(buf, N, {N});
+      made[0] = piece(buf, 2 * N, {B + 1});
+      made[4] = piece(buf, 2 * N + B + 1, {2});
       if (tree) made[3] = c.empty({N}, at::kLong);
       a.slots = static_cast<int32_t*>(buf.data_ptr());
       a.positions = a.slots + N;
@@ -380,10 +391,10 @@ PyObject* token_logprobs(PyObject*, PyObject* const* o, Py_ssize_t n) {
     }
     PyObject* out = PyTuple_New(4);
     if (!out) return nullptr;
-    PyTuple_SET_ITEM(out, 0, wrap(buf.narrow(0, 0, T * N).view({T, N})));
-    PyTuple_SET_ITEM(out, 1, wrap(buf.narrow(0, T * N, T)));
+    PyTuple_SET_ITEM(out, 0, wrap(piece(buf, 0, {T, N})));
+    PyTuple_SET_ITEM(out, 1, wrap(piece(buf, T * N, {T})));
     PyTuple_SET_ITEM(out, 2, wrap(ids));
-    PyTuple_SET_ITEM(out, 3, wrap(buf.narrow(0, T * (N + 1), T * top).view({T, top})));
+    PyTuple_SET_ITEM(out, 3, wrap(piece(buf, T * (N + 1), {T, top})));
     return out;
   });
 }
