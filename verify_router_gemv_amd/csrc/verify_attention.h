@@ -34,7 +34,9 @@
 namespace verify {
 
 constexpr int kTile = 32;          // tokens per step of a wave
-constexpr int kMinTiles = 4;       // fewest tiles per wave a context is split down to
+// A context of more than kSplitTiles tiles per wave of a block is split, into parts of at least kMinTiles: a
+// tile more costs a wave about 2 us of latency, a split the second kernel, 5 us.
+constexpr int kSplitTiles = 4, kMinTiles = 2;
 constexpr int kCus = 256;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -46,7 +48,8 @@ struct AttnLaunch {
   int32_t m_shift;   // log2 of the query rows (rows * group) per block
   int32_t target;    // blocks to spread the work over, all heads together
   int32_t grid;      // blocks launched
-  int32_t least;     // fewest tiles of a part
+  int32_t least;     // fewest tiles of a part ...
+  int32_t whole;     // ... and most of a context that is not split for the sake of the chip's width
   int32_t swizzle;   // 1: several row blocks per request, kept on one XCD (8 neighbours)
   float* part;       // [grid][rows][D] partial outputs, then [grid][rows][2] (maximum, sum)
   int32_t* plan;     // [B][2] first block and number of parts of each request, for the join
@@ -108,7 +111,8 @@ __device__ __forceinline__ bool attn_item(const verify_attention_args& a, const 
     const int b = b0 + lane;
     if (a.n_requests > 64) q = b < a.n_requests ? attn_request(a, b) : AttnRequest{0, 0, 0, 0};
     const unsigned tiles = static_cast<unsigned>(q.len + kTile - 1) / kTile;
-    const int parts = tiles > chunk ? static_cast<int>((tiles + chunk - 1) / chunk) : 1;
+    const bool split = tiles > max(chunk, static_cast<unsigned>(p.whole));
+    const int parts = split ? static_cast<int>((tiles + chunk - 1) / chunk) : 1;
     const int mbs = (q.rows * group + rnd) >> p.m_shift;
     int units = parts * a.kv_heads;
     if (p.swizzle) units = (units + 7) & ~7;
@@ -726,7 +730,9 @@ inline bool attn_plan(const verify_attention_args& a, AttnLaunch* p, int64_t* by
   const int m = a.max_rows * (a.heads / a.kv_heads), rows = 32 * attn_wm(a);
   const int64_t per_request = (m + rows - 1) / rows;
   p->m_shift = __builtin_ctz(rows);
-  p->least = kMinTiles * ((a.dim == 256 ? 4 : 8) / (rows / 32));
+  const int wk = (a.dim == 256 ? 4 : 8) / (rows / 32);
+  p->least = kMinTiles * wk;
+  p->whole = kSplitTiles * wk;
   p->swizzle = per_request > 1;
   // Each (row block, head) rounds up to a whole number of parts, so the call makes up to `once` blocks more
   // than the target. While that leaves room, all blocks fit the chip at once; with more, the target is
@@ -738,8 +744,8 @@ inline bool attn_plan(const verify_attention_args& a, AttnLaunch* p, int64_t* by
   p->grid = static_cast<int32_t>(grid);
   p->part = nullptr;
   p->plan = nullptr;
-  // A table that holds no more tokens than the least part never splits.
-  const bool split = static_cast<int64_t>(a.width) * a.page_size > p->least * kTile;
+  // A table that holds no more than that never splits.
+  const bool split = static_cast<int64_t>(a.width) * a.page_size > p->whole * kTile;
   *bytes = split ? grid * rows * (a.dim + 2) * 4 + a.n_requests * 8 : 0;
   return true;
 }
