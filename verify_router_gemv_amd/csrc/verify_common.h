@@ -80,11 +80,6 @@ __device__ __forceinline__ int wave_max(int v) {
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return max(static_cast<int>(b[0]), static_cast<int>(b[1]));
 }
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v = min(v, __shfl_xor(v, s));
-  return v;
-}
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }

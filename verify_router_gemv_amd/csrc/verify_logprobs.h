@@ -8,11 +8,15 @@
 // the wave then takes the chunk's best elements out one by one, largest first, so a chunk costs at most K
 // insertions, and a random row about K ln(n / K) in all.
 //
-// All rows' chunks of 1024 logits form one sequence that is cut evenly over the waves the chip holds, so
-// every wave reads the same amount whatever the rows and the vocabulary are; a wave that crosses from one
-// row into the next writes a part per row, and a second kernel joins each row's parts (one wave a row).
+// All rows' chunks of 1024 logits form one sequence that is cut evenly over the waves the chip holds (a
+// chunk is not cut: a wave's second chunk costs 2.5 us with 8 alternatives, its list in the second kernel
+// less), so every wave reads the same amount whatever the rows and the vocabulary are; a wave that crosses
+// from one row into the next writes a part per row, and a second kernel joins each row's parts.
 // Bound: memory from a few dozen rows of 10^5 logits (a 16-bit row is near the vector rate too, about
 // twelve issue slots an element); below, launch, load and insertion latency.
+// Measured, first kernel + join: 2048 rows of 131072 bf16, 1 alternative, 98 + 4.9 us (5.5 TB/s; with 8
+// alternatives 112 + 4.9); 24 rows of 151001 bf16, 8 alternatives, 9.8 + 7.4; one row of 248000 fp32, 8
+// alternatives, 6.4 + 6.8 (4.3 + 2.5 without).
 #pragma once
 
 #include "verify_common.h"
@@ -101,7 +105,7 @@ __device__ __forceinline__ void lp_first(LpTop& top, int key, int id, int K, int
     int from = __ffsll(static_cast<unsigned long long>(who)) - 1;
     int lo = __builtin_amdgcn_readlane(id, from);
     if (who & (who - 1)) {  // equal ones
-      lo = uniform(wave_min(key == w ? id : INT32_MAX));
+      lo = ~uniform(wave_max(key == w ? ~id : INT32_MIN));
       from = __ffsll(static_cast<unsigned long long>(__ballot(key == w && id == lo))) - 1;
     }
     top.k = lane == i ? w : top.k;
@@ -132,27 +136,40 @@ __device__ __forceinline__ int lp_place(int j, int lane) {
 }
 
 // Takes those of a chunk's elements that are among the best K: x the lanes' elements (NaN: none), best their
-// largest, base the id of the chunk's first. With a list that is not full, or with many lanes that have
-// something to offer, the lanes' best elements go first: the K best of them are a list already, or raise
-// the cut, so that little is left to insert one by one, whatever the order of the row.
+// largest, base the id of the chunk's first. Every lane offers its best element, then its second best, until
+// none is good enough. With a list that is not full, or with many lanes that have something to offer, the
+// first offers go as a list of their own: its K are a list already, or raise the cut, so that little is left
+// to insert one by one, whatever the order of the row. (One loop, not one branch per element: the code is
+// fetched anew in each launch, and sixteen skipped copies of the insertion cost more than the work.)
 template <int VEC>
-__device__ __forceinline__ void lp_take(LpTop& top, const float (&x)[kLpEach], float best, int K, int lane, int base) {
-  int done = -1;  // the lane's element that has gone first
-  if (top.n < K || __popcll(__ballot(lp_key(best) > top.cut)) > 4 + K) {
+__device__ __forceinline__ void lp_take(LpTop& top, float (&x)[kLpEach], float best, int K, int lane, int base) {
+  for (;;) {
+    const int key = lp_key(best);
+    int at = 0;  // the lane's first element that is its best
 #pragma unroll
-    for (int j = kLpEach - 1; j >= 0; --j) done = x[j] == best ? j : done;
-    LpTop mine;
-    lp_first(mine, lp_key(best), base + lp_place<VEC>(done, lane), K, lane);
-    if (top.n == 0) top = mine;
-    else lp_each(top, (uint64_t(1) << mine.n) - 1, mine.k, mine.id, K, lane);
-  }
+    for (int j = kLpEach - 1; j >= 0; --j) at = x[j] == best ? j : at;
+    const int id = base + lp_place<VEC>(at, lane);
+    uint64_t who = __ballot(key != kLpNone && lp_good(top, key, id, K));
+    if (!who) break;
+    int ok = key, oi = id;  // what is offered
+    if (top.n < K || __popcll(who) > 4 + K) {
+      LpTop mine;
+      lp_first(mine, key, id, K, lane);
+      ok = mine.k;
+      oi = mine.id;
+      who = (uint64_t(1) << mine.n) - 1;
+      if (top.n == 0) {
+        top = mine;
+        who = 0;
+      }
+    }
+    lp_each(top, who, ok, oi, K, lane);
+    best = __builtin_nanf("");
 #pragma unroll
-  for (int j = 0; j < kLpEach; ++j) {
-    const float least = top.n < K ? kLpNegInf : lp_unkey(top.cut);
-    const bool may = x[j] >= least;
-    if (!__ballot(may)) continue;
-    const int id = base + lp_place<VEC>(j, lane), key = lp_key(x[j]);
-    lp_each(top, __ballot(may && j != done && lp_good(top, key, id, K)), key, id, K, lane);
+    for (int j = 0; j < kLpEach; ++j) {
+      x[j] = j == at ? __builtin_nanf("") : x[j];
+      best = fmaxf(best, x[j]);
+    }
   }
 }
 
@@ -281,9 +298,16 @@ __global__ void __launch_bounds__(kLpThreads, lp_waves(sizeof(T))) logprobs_kern
   }
 }
 
+// One block a row, of a wave per 64 parts up to kJoinWaves; the first wave joins what the waves found.
+constexpr int kJoinWaves = 4;
+static_assert(kJoinWaves * kTop <= 64, "their lists' entries lie in one wave");
+
 template <typename T>
-__global__ void __launch_bounds__(64) logprobs_join_kernel(verify_logprobs_args a, LpPlan p) {
-  const int lane = threadIdx.x, t = blockIdx.x, K = a.top;
+__global__ void __launch_bounds__(64 * kJoinWaves) logprobs_join_kernel(verify_logprobs_args a, LpPlan p) {
+  __shared__ LpStat stats[kJoinWaves];
+  __shared__ int keys[kJoinWaves * kTop], ids[kJoinWaves * kTop];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int t = blockIdx.x, K = a.top;
   const T* const row = static_cast<const T*>(a.logits) + t * a.row_stride;
   // The given tokens' logits, asked for first.
   const int64_t tok0 = static_cast<int64_t>(t) * a.n_tokens;
@@ -293,7 +317,7 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(verify_logprobs_args 
   };
   int64_t id0 = -1;
   float x0 = 0;
-  if (lane < a.n_tokens) {
+  if (wave == 0 && lane < a.n_tokens) {
     id0 = token(lane);
     if (id0 >= 0 && id0 < a.vocab) x0 = static_cast<float>(row[id0]);
   }
@@ -304,35 +328,57 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(verify_logprobs_args 
   const int parts = static_cast<int>(w1 - w0 + 1);
   const int64_t at0 = w0 + t;
   LpStat st{kLpNegInf, 0, 0};
-  for (int i = lane; i < parts; i += 64)
+  const bool flat = waves == 1 && parts * K <= 64;  // the lists' entries, one a lane
+  int fk = kLpNone, fid = -1;
+  if (flat && lane < parts * K) {
+    fk = p.tk[at0 * K + lane];
+    fid = p.ti[at0 * K + lane];
+  }
+  for (int i = 64 * wave + lane; i < parts; i += 64 * waves)
     st = lp_join(st, LpStat{p.stat[3 * (at0 + i)], p.stat[3 * (at0 + i) + 1], p.stat[3 * (at0 + i) + 2]});
-  st = lp_wave(st);
-  // The lists are sorted: the best of each first, then the second best, until none is good enough. All of
-  // 64 lists are asked for at once.
   LpTop top;
-  for (int i0 = 0; i0 < parts && K; i0 += 64) {
-    const int i = i0 + lane;
-    int k[kTop], id[kTop];
+  if (flat) {
+    if (K) lp_first(top, fk, fid, K, lane);
+  } else {
+    // The lists are sorted: the best of each first, then the second best, until none is good enough. All of
+    // 64 lists are asked for at once.
+    for (int i0 = 64 * wave; i0 < parts && K; i0 += 64 * waves) {
+      const int i = i0 + lane;
+      int k[kTop], id[kTop];
 #pragma unroll
-    for (int r = 0; r < kTop; ++r) {
-      k[r] = kLpNone;
-      if (r < K && i < parts) {
-        k[r] = p.tk[(at0 + i) * K + r];
-        id[r] = p.ti[(at0 + i) * K + r];
+      for (int r = 0; r < kTop; ++r) {
+        k[r] = kLpNone, id[r] = -1;
+        if (r < K && i < parts) {
+          k[r] = p.tk[(at0 + i) * K + r];
+          id[r] = p.ti[(at0 + i) * K + r];
+        }
+      }
+      const bool first = i0 == 64 * wave;
+      if (first) lp_first(top, k[0], id[0], K, lane);
+      for (int r = first; r < K; ++r) {
+        if (r) {  // the next of each list, to the front
+#pragma unroll
+          for (int q = 0; q + 1 < kTop; ++q) k[q] = k[q + 1], id[q] = id[q + 1];
+        }
+        const uint64_t who = __ballot(k[0] != kLpNone && lp_good(top, k[0], id[0], K));
+        if (!who) break;
+        lp_each(top, who, k[0], id[0], K, lane);
       }
     }
-    int r0 = 0;
-    if (i0 == 0) {
-      lp_first(top, k[0], id[0], K, lane);
-      r0 = 1;
+  }
+  st = lp_wave(st);
+  if (waves > 1) {
+    if (lane == 0) stats[wave] = st;
+    if (lane < kTop) {
+      keys[wave * kTop + lane] = lane < top.n ? top.k : kLpNone;
+      ids[wave * kTop + lane] = top.id;
     }
-#pragma unroll
-    for (int r = 0; r < kTop; ++r) {
-      if (r < r0 || r >= K) continue;
-      const uint64_t who = __ballot(k[r] != kLpNone && lp_good(top, k[r], id[r], K));
-      if (!who) break;
-      lp_each(top, who, k[r], id[r], K, lane);
-    }
+    __syncthreads();
+    if (wave) return;
+    st = lp_wave(lane < waves ? stats[lane] : LpStat{kLpNegInf, 0, 0});
+    top = LpTop{};
+    const int at = lane < waves * kTop ? lane : 0;
+    if (K) lp_first(top, lane < waves * kTop ? keys[at] : kLpNone, ids[at], K, lane);
   }
 
   const float lg = __builtin_amdgcn_logf(st.l);  // log2
@@ -362,7 +408,6 @@ inline LpPlan lp_plan(const verify_logprobs_args& a, void* workspace, int64_t* b
   const int64_t all = static_cast<int64_t>(a.n_rows) * p.chunks;
   const int64_t resident = 256 * 4 * lp_waves(a.type == VERIFY_F32 ? 4 : 2);
   p.per_wave = (all + resident - 1) / resident;
-  if (p.per_wave < 2) p.per_wave = 2;
   p.waves = (all + p.per_wave - 1) / p.per_wave;
   const int64_t parts = p.waves + a.n_rows;
   *bytes = parts * (12 + 8 * a.top);
@@ -377,7 +422,9 @@ hipError_t launch_logprobs_t(const verify_logprobs_args& a, const LpPlan& p, hip
   logprobs_kernel<T><<<dim3(static_cast<unsigned>((p.waves + kLpWaves - 1) / kLpWaves)), kLpThreads, 0, stream>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  logprobs_join_kernel<T><<<dim3(a.n_rows), 64, 0, stream>>>(a, p);
+  const int64_t parts = (p.chunks - 1) / p.per_wave + 2;  // of a row, at most
+  const int waves = static_cast<int>(parts >= 64 * kJoinWaves ? kJoinWaves : (parts + 63) / 64);
+  logprobs_join_kernel<T><<<dim3(a.n_rows), 64 * waves, 0, stream>>>(a, p);
   return hipGetLastError();
 }
 
