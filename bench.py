@@ -47,7 +47,7 @@ def parse():
                    help="skip the kernel-timing pass (no roofline)")
     p.add_argument("--prefill-only", type=int, default=0, metavar="T",
                    help="only the prefill section, at T rows (for profiling it); prints its JSON")
-    p.add_argument("--only", default="", choices=("", "decode", "wide", "deep", "tier", "launch", "choices"),
+    p.add_argument("--only", default="", choices=("", "decode", "wide", "deep", "tier", "launch", "choices", "round"),
                    help="only that extra section (for profiling it); prints its JSON")
     return p.parse_args()
 
@@ -95,7 +95,8 @@ def main():
                    "deep": lambda: deep_stack(torch, np, synth, MoeRound),
                    "tier": lambda: tier_rounds(torch, np, synth, MoeRound),
                    "launch": lambda: launch_costs(torch, np, synth, MoeRound),
-                   "choices": lambda: launch_choices(cfg, base, torch, np, MoeRound)}[args.only]
+                   "choices": lambda: launch_choices(cfg, base, torch, np, MoeRound),
+                   "round": lambda: whole_round(cfg, base, torch, np, MoeRound)}[args.only]
         print(json.dumps({args.only: run_one()}), flush=True)
         return
     reps = [base] + [base.clone() for _ in range(args.replicas - 1)]
@@ -720,6 +721,86 @@ def launch_costs(torch, np, synth, MoeRound):
         res[f"{name}_kernels_us_per_launch_by_blocks"] = per_blocks
         res[f"{name}_ns_per_block"] = round((per_blocks["1024"] - per_blocks["1"]) / 1023 * 1e3, 1)
     h.close()
+    return res
+
+
+def whole_round(cfg, layer, torch, np, MoeRound, heads=32, kv_heads=4, dim=128, page=64, vocab=151001, replicas=8):
+    """The verify round around its MoE: slots and tree masks once, per layer the norm, rotary position and
+    cache write, the attention and the MoE round, then the log probabilities. 8 requests of T = 1, 3 or 8
+    drafted rows each over 2000 to 8192 tokens of context; the projections, which are library products, are
+    left out (their results stand ready). Each layer has its own cache and weights, so that none of them
+    comes from the Infinity Cache. Median us of a round of `replicas` layers, eager and captured, and of
+    its parts, each alone and synchronised (launch included)."""
+    import verify_router_gemv_amd as v
+
+    dev, B, width = layer.router_w.device, 8, 8192 // page + 1
+    rng = np.random.default_rng(0)
+    g = torch.Generator(device=dev).manual_seed(0)
+    half = dict(generator=g, device=dev, dtype=torch.bfloat16)
+    caches = [[torch.randn(B * width, kv_heads, page, dim, **half) for _ in range(2)] for _ in range(replicas)]
+    i32 = lambda a: torch.as_tensor(np.asarray(a), dtype=torch.int32, device=dev)
+    cached = i32(rng.integers(2000, 8192, B))
+    inv_freq = (1e6 ** (-torch.arange(0, dim, 2, device=dev).double() / dim)).float()
+    norm = torch.ones(dim, device=dev)
+    res = {"requests": B, "context": "2000-8192", "layers": replicas, "timing": "torch events, median of 50"}
+    for T in TS:
+        N = B * T
+        rows, parents = i32([T] * B), i32([p for _ in range(B) for p in range(-1, T - 1)])
+        pages = rng.permutation(B * width).reshape(B, width)
+        table, free = i32(pages), i32([0])  # the pages the round grows into are in the table already
+        qkv = torch.randn(N, heads + 2 * kv_heads, dim, **half)
+        q, k, val = qkv.split([heads, kv_heads, kv_heads], 1)
+        qo, att = torch.empty_like(q.contiguous()), torch.empty(N, heads, dim, device=dev, dtype=torch.bfloat16)
+        x = torch.randn(N, cfg.H, generator=g, device=dev)
+        out = torch.empty_like(x)
+        logits = torch.randn(N, vocab, **half)
+        drafted = torch.randint(vocab, (N, 1), generator=g, device=dev)
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            moe = [MoeRound([layer.clone()], cfg.H, cfg.I, cfg.E, cfg.k, max_rows=64, use_graph=False, stream=stream)
+                   for _ in range(replicas)]
+            slots = v.round_slots(cached, rows, table, free, page, N, parents)
+            parts = {
+                "round_slots": lambda l: v.round_slots(cached, rows, table, free, page, N, parents, out=slots),
+                "qk_norm_rope": lambda l: v.qk_norm_rope(q, k, val, slots.positions, slots.slots, inv_freq, *caches[l], qo,
+                                                         q_weight=norm, k_weight=norm),
+                "tree_attention": lambda l: v.tree_attention(qo, *caches[l], table, cached, slots.row_start,
+                                                             masks=slots.masks, max_rows=T, out=att),
+                "moe_round": lambda l: moe[l].run(x, cfg.k, out),
+                "token_logprobs": lambda l: v.token_logprobs(logits, drafted, top=8),
+            }
+
+            def one_round():
+                parts["round_slots"](0)
+                for l in range(replicas):
+                    for name in ("qk_norm_rope", "tree_attention", "moe_round"):
+                        parts[name](l)
+                return parts["token_logprobs"](0)
+
+            for _ in range(3):
+                one_round()
+            torch.cuda.synchronize()
+            med = lambda fn, n=50: round(float(np.median([event_us(torch, fn) for _ in range(n)])), 1)
+            at = [0]
+
+            def next_layer(fn):
+                at[0] = (at[0] + 1) % replicas
+                fn(at[0])
+
+            per = {"eager": med(one_round)}
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                kept = one_round()
+            graph.replay()
+            per["captured"] = med(graph.replay)
+            for name, fn in parts.items():
+                per[name] = med(lambda: next_layer(fn))
+            del graph, kept
+            for h in moe:
+                h.close()
+        torch.cuda.current_stream().wait_stream(stream)
+        res[f"T{T}_us"] = per
     return res
 
 
