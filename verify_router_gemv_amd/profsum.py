@@ -1,7 +1,7 @@
 """Short text summaries of rocprofv3 output for the round's kernels.
 
     python -m verify_router_gemv_amd.profsum stats  STATS_CSV OUT "COMMAND"
-        per-kernel dispatch durations (calls, average, min, max) of the moe:: kernels from a
+        per-kernel dispatch durations (calls, average, min, max) of the library's kernels from a
         `rocprofv3 --kernel-trace --stats` *_kernel_stats.csv
     python -m verify_router_gemv_amd.profsum traffic FETCH_DIR WRITE_DIR OUT "COMMAND" [KERNEL]
         gate/up HBM traffic per dispatch from a FETCH_SIZE pass and a WRITE_SIZE pass of
@@ -15,6 +15,7 @@ import csv
 import glob
 import hashlib
 import os
+import re
 import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -58,12 +59,24 @@ def read_traffic(path: str, kernel: str = "gateup"):
     return int(float(kv["traffic_bytes_per_launch"]))
 
 
+def kernel_name(n: str):
+    """The short name of a kernel of the library, None for another's. (Names with 16-bit types come as the
+    compiler writes them.)"""
+    m = re.match(r"_ZN6verify\d+([a-z_]+)I(\w+?)EEv", n)
+    if m:
+        types = {"DF16b": "bf16", "DF16_": "fp16", "f": "fp32"}
+        args = re.finditer(r"DF16b|DF16_|f|Li(\d+)E", m.group(2) + "E")
+        return f"{m.group(1)}<{', '.join(a.group(1) or types[a.group()] for a in args)}>"
+    if "moe::" in n or "verify::" in n:
+        return n.split("(")[0].replace("void ", "").replace("moe::", "", 1).replace("verify::", "", 1)
+    return None
+
+
 def stats(stats_csv: str, out_path: str, command: str) -> None:
     rows = []
     for r in csv.DictReader(open(stats_csv)):
-        n = r["Name"]
-        if "moe::" in n:  # the library's kernels (input generation and copies are left out)
-            short = n.split("(")[0].replace("void moe::", "")
+        short = kernel_name(r["Name"])
+        if short:  # the library's kernels (input generation and copies are left out)
             rows.append((short, int(r["Calls"]), float(r["AverageNs"]) / 1e3, float(r["MinNs"]) / 1e3,
                          float(r["MaxNs"]) / 1e3, float(r["Percentage"])))
     rows.sort(key=lambda x: -x[1] * x[2])
