@@ -21,6 +21,8 @@
  * must be the stream's; lengths, tables and masks are read on the GPU when the call executes, so a
  * captured graph follows their contents.  `stream` is a hipStream_t, NULL the null stream.
  *
+ * Outputs may not share memory with inputs or with each other unless a call says so.
+ *
  * Contents that cannot be checked without waiting for the GPU are bounded there: no index read from
  * device memory is followed outside its array (see each call for what happens instead).
  *
@@ -159,11 +161,13 @@ MOE_ROUND_API moe_status verify_qk_norm_rope(const verify_rope_args* a, void* st
  * float32, each probability rounded to the cache's type for its product with the values (relative to
  * the row's running maximum), the output rounded once.
  * Results do not depend on timing (no atomics); how the context is split depends on the lengths of all
- * requests of the call, and changes results by float32 rounding only.
+ * requests of the call, and changes results within the rounding of the probabilities (each part has its
+ * own running maximum).
  *
  * Supported: D 64, 128 or 256; heads a multiple of kv_heads; P a power of two from 16 to 65536; max_rows
  * 1..VERIFY_MAX_TREE_ROWS; heads / kv_heads up to 64; type VERIFY_BF16 or VERIFY_F16 (q, cache and out
- * alike); pointers 16-byte aligned, strides multiples of 16 bytes; scale > 0; out may be q itself.
+ * alike); pointers 16-byte aligned, strides multiples of 16 bytes; scale > 0; out may be q itself (the
+ * same strides; any other overlap of the two is refused).
  * `workspace` is device memory of at least verify_tree_attention_workspace(a) bytes (0 if none is
  * needed), 16-byte aligned, free for other use when the call has executed; its contents do not matter.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP.  n_rows = 0 or n_requests = 0: nothing is

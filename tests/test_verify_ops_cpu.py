@@ -141,6 +141,8 @@ BAD = [
     ("attention", dict(q=0), INVALID), ("attention", dict(out=P16 + 8), INVALID), ("attention", dict(masks=P16 + 4), INVALID),
     ("attention", dict(o_row=0), INVALID), ("attention", dict(kc_token=132), INVALID), ("attention", dict(table=0), INVALID),
     ("attention", dict(cached=0), INVALID), ("attention", dict(row_start=P16 + 2), INVALID),
+    ("attention", dict(width=64, out=P16 + 256), INVALID),               # overlaps q (no workspace is needed)
+    ("attention", dict(width=64, o_row=1024), INVALID),                  # q itself, other strides
     ("attention", dict(), INVALID),                                      # the context may split: no workspace given
     ("attention", dict(dim=80), UNSUPPORTED), ("attention", dict(type=0), UNSUPPORTED),
     ("attention", dict(page_size=8), UNSUPPORTED), ("attention", dict(page_size=48), UNSUPPORTED),

@@ -19,6 +19,16 @@ static bool apart(int64_t s, int64_t n) { return s > 0 || n <= 1; }
 constexpr int64_t kWide = int64_t(1) << 40;   // rows, heads and pages: 64-bit products
 constexpr int64_t kNear = int64_t(1) << 24;   // tokens of a page: 32-bit products with up to 15
 
+// An output over the queries: the same elements, or none.
+static bool over_ok(const void* q, int q_type, int64_t q_row, int64_t q_head, const void* out, int o_type, int64_t o_row,
+                    int64_t o_head, int64_t rows, int64_t heads, int64_t dim) {
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  if (q0 == o0) return q_type == o_type && q_row == o_row && q_head == o_head;
+  const uintptr_t q1 = q0 + ((rows - 1) * q_row + (heads - 1) * q_head + dim) * size_of(q_type);
+  const uintptr_t o1 = o0 + ((rows - 1) * o_row + (heads - 1) * o_head + dim) * size_of(o_type);
+  return q0 >= o1 || o0 >= q1;
+}
+
 moe_status validate_slots(const verify_slots_args* a) {
   if (!a || a->struct_bytes != static_cast<int64_t>(sizeof(*a)) || a->reserved) return MOE_ERR_INVALID_ARG;
   if (a->n_requests < 0 || a->width < 1 || a->n_free < 0 || a->page_size < 1 || a->total_rows < 0 ||
@@ -64,16 +74,9 @@ moe_status validate_rope(const verify_rope_args* a) {
       !good(a->v_cache, 16) || !good(a->positions, 4) || !good(a->slots, 4) || !aligned(a->q_weight, 16) ||
       !aligned(a->k_weight, 16) || (a->n_freq > 0 && !good(a->inv_freq, 4)))
     return MOE_ERR_INVALID_ARG;
-  // q_out over q: the same elements, or none
-  const uintptr_t q0 = reinterpret_cast<uintptr_t>(a->q), o0 = reinterpret_cast<uintptr_t>(a->q_out);
-  if (q0 == o0) {
-    if (a->in_type != a->cache_type || a->q_row != a->o_row || a->q_head != a->o_head) return MOE_ERR_INVALID_ARG;
-  } else {
-    const int64_t rows = a->n_rows - 1, heads = a->heads - 1;
-    const uintptr_t q1 = q0 + (rows * a->q_row + heads * a->q_head + a->dim) * in;
-    const uintptr_t o1 = o0 + (rows * a->o_row + heads * a->o_head + a->dim) * out;
-    if (q0 < o1 && o0 < q1) return MOE_ERR_INVALID_ARG;
-  }
+  if (!over_ok(a->q, a->in_type, a->q_row, a->q_head, a->q_out, a->cache_type, a->o_row, a->o_head, a->n_rows, a->heads,
+               a->dim))
+    return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -100,6 +103,8 @@ moe_status validate_attention(const verify_attention_args* a) {
   if (a->n_rows == 0 || a->n_requests == 0) return MOE_OK;
   if (!good(a->q, 16) || !good(a->out, 16) || !good(a->k_cache, 16) || !good(a->v_cache, 16) || !good(a->table, 4) ||
       !good(a->cached, 4) || !good(a->row_start, 4) || !aligned(a->masks, 8))
+    return MOE_ERR_INVALID_ARG;
+  if (!over_ok(a->q, a->type, a->q_row, a->q_head, a->out, a->type, a->o_row, a->o_head, a->n_rows, a->heads, a->dim))
     return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }

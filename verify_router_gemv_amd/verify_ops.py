@@ -8,9 +8,9 @@
 As with the MoE round's binding, tensors are checked (types, shapes, devices), raw device pointers passed
 and status codes mapped to exceptions, here by the extension module _verify_ops (csrc/verify_binding.cpp);
 what is computed is computed in the HIP library, and include/verify_ops.h has each call's definition and
-limits.  All calls are asynchronous on the current
-stream of the tensors' device and may be captured into a graph.  Outputs that are not given are
-allocated, as is the scratch memory (from torch's allocator, on that stream).
+limits.  All calls are asynchronous on the current stream of the tensors' device and may be captured into a
+graph.  Outputs that are not given are allocated, as is the scratch memory (from torch's allocator, on that
+stream).  They serve: no call records a gradient, whatever its inputs require.
 """
 from __future__ import annotations
 
