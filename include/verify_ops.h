@@ -48,7 +48,7 @@ extern "C" {
 
 #define VERIFY_MAX_TREE_ROWS 64      /* rows of one request in a tree (bits of a mask word)   */
 #define VERIFY_MAX_REQUESTS 65536    /* B                                                     */
-#define VERIFY_MAX_TOTAL_ROWS 16777216 /* rows of one call                                    */
+#define VERIFY_MAX_TOTAL_ROWS 16777215 /* rows of one call: a block of 256 each, below 2^32 threads */
 #define VERIFY_MAX_ALTERNATIVES 16   /* top alternatives per row                              */
 
 /*
@@ -60,7 +60,7 @@ extern "C" {
  * are taken from `free_pages` in request order, starting at *free_head, and written into the table (all
  * other table entries stay as they are).  Row i of request b is token c_b + i of the cache:
  *   slots[S_b + i]     = table[b][(c_b + i) / P] * P + (c_b + i) % P
- *   positions[S_b + i] = c_b + depth(i)
+ *   positions[S_b + i] = c_b + depth(i)     (at most 2^31 - 1)
  *   masks[S_b + i]     = bit i, and the bits of all of row i's ancestors
  * With `parents`, parents[S_b + i] in -1 .. i - 1 is the row of the same request that row i hangs
  * below (-1, or any value outside that range: directly below the cached tokens) and depth counts row
@@ -167,7 +167,9 @@ MOE_ROUND_API moe_status verify_qk_norm_rope(const verify_rope_args* a, void* st
  * Supported: D 64, 128 or 256; heads a multiple of kv_heads; P a power of two from 16 to 65536; max_rows
  * 1..VERIFY_MAX_TREE_ROWS; heads / kv_heads up to 64; type VERIFY_BF16 or VERIFY_F16 (q, cache and out
  * alike); pointers 16-byte aligned, strides multiples of 16 bytes; scale > 0; out may be q itself (the
- * same strides; any other overlap of the two is refused).
+ * same strides; any other overlap of the two is refused). A launch of 2^32 threads or more is refused
+ * (MOE_ERR_UNSUPPORTED): n_rows * heads above 2^26 - 4 where the context may be split, or some millions of
+ * blocks of 32 to 256 query rows of one kv head.
  * `workspace` is device memory of at least verify_tree_attention_workspace(a) bytes (0 if none is
  * needed), 16-byte aligned, free for other use when the call has executed; its contents do not matter.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP.  n_rows = 0 or n_requests = 0: nothing is

@@ -5,7 +5,7 @@ import torch
 
 import verify_router_gemv_amd as v
 from oracle import verify_oracle
-from verify_helpers import DEV, i32, random_parents, say
+from verify_helpers import DEV, host, i32, random_parents, say
 
 pytestmark = pytest.mark.gpu
 
@@ -92,6 +92,17 @@ def test_what_does_not_fit_is_left_out():
     check(cached, new, table, free, 16, N, bad, what="parents out of range")
     table[3, 0] = -1
     check(cached, new, table, free, 16, N, what="a missing page in the table")
+
+
+def test_lengths_at_the_end_of_32_bits():
+    last = 2 ** 31 - 1
+    cached, new = np.array([last, last - 3, 5], np.int32), np.array([4, 8, 2], np.int32)
+    table, free, N = i32(np.zeros((3, 4))), i32(np.arange(4)), 15
+    for parents in (None, i32([-1, 0, 1, 2, -1, 0, 1, 2, 3, 4, 5, 6, -1, 0, -1])):
+        s = v.round_slots(i32(cached), i32(new), table.clone(), free, 16, N, parents)
+        want = [min(int(c) + i, last) for c, n in zip(cached, new) for i in range(n)] + [0]
+        assert host(s.positions).tolist() == want
+        assert (host(s.slots)[:12] == -1).all() and host(s.slots)[12:14].tolist() == [5, 6]
 
 
 def test_more_than_64_rows_in_a_tree():

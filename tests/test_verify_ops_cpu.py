@@ -120,7 +120,8 @@ BAD = [
     ("slots", dict(slots=0), INVALID), ("slots", dict(counts=0), INVALID), ("slots", dict(row_start=0), INVALID),
     ("slots", dict(masks=P16 + 4), INVALID), ("slots", dict(free_head=P16 + 1), INVALID),
     ("slots", dict(n_requests=65537), UNSUPPORTED), ("slots", dict(page_size=65537), UNSUPPORTED),
-    ("slots", dict(total_rows=16777217), UNSUPPORTED),
+    ("slots", dict(total_rows=16777217), UNSUPPORTED), ("slots", dict(total_rows=16777216), UNSUPPORTED),
+    ("rope", dict(n_rows=16777216), UNSUPPORTED), ("logprobs", dict(n_rows=16777216), UNSUPPORTED),
     ("rope", dict(struct_bytes=0), INVALID), ("rope", dict(heads=0), INVALID), ("rope", dict(kv_heads=0), INVALID),
     ("rope", dict(n_pages=0), INVALID), ("rope", dict(page_size=0), INVALID), ("rope", dict(eps=-1.0), INVALID),
     ("rope", dict(eps=math.nan), INVALID), ("rope", dict(eps=math.inf), INVALID), ("rope", dict(interleaved=2), INVALID),
@@ -147,6 +148,8 @@ BAD = [
     ("attention", dict(dim=80), UNSUPPORTED), ("attention", dict(type=0), UNSUPPORTED),
     ("attention", dict(page_size=8), UNSUPPORTED), ("attention", dict(page_size=48), UNSUPPORTED),
     ("attention", dict(max_rows=65), UNSUPPORTED), ("attention", dict(heads=130), UNSUPPORTED),
+    ("attention", dict(n_rows=1 << 20, heads=64, kv_heads=1, q=1 << 40), UNSUPPORTED),          # the join's threads
+    ("attention", dict(width=64, n_requests=65536, max_rows=64, heads=1024, kv_heads=64, q=1 << 40), UNSUPPORTED),  # the blocks
     ("attention", dict(width=1 << 27, table_stride=1 << 27), UNSUPPORTED),
     ("logprobs", dict(struct_bytes=80), INVALID), ("logprobs", dict(vocab=0), INVALID), ("logprobs", dict(n_tokens=-1), INVALID),
     ("logprobs", dict(row_stride=999), INVALID), ("logprobs", dict(tokens_64=2), INVALID), ("logprobs", dict(logits=0), INVALID),

@@ -725,7 +725,7 @@ inline int attn_wm(const verify_attention_args& a) {
   return wm;
 }
 
-// The grid and the workspace of a call; false if the blocks do not fit 31 bits.
+// The grid and the workspace of a call; false if a launch would reach 2^32 threads.
 inline bool attn_plan(const verify_attention_args& a, AttnLaunch* p, int64_t* bytes) {
   const int m = a.max_rows * (a.heads / a.kv_heads), rows = 32 * attn_wm(a);
   const int64_t per_request = (m + rows - 1) / rows;
@@ -742,12 +742,14 @@ inline bool attn_plan(const verify_attention_args& a, AttnLaunch* p, int64_t* by
   const int64_t row_blocks = static_cast<int64_t>(a.n_requests) * per_request, once = row_blocks * a.kv_heads;
   p->target = static_cast<int32_t>(once <= kCus / 2 ? kCus - once : 2 * kCus);
   const int64_t grid = p->target + once + (p->swizzle ? 7 * row_blocks : 0) + 8;
-  if (grid > INT32_MAX) return false;
+  constexpr int64_t kThreads = UINT32_MAX;
+  if (grid > kThreads / 512) return false;
   p->grid = static_cast<int32_t>(grid);
   p->part = nullptr;
   p->plan = nullptr;
   // A table that holds no more than that never splits.
   const bool split = static_cast<int64_t>(a.width) * a.page_size > p->whole * kTile;
+  if (split && (static_cast<int64_t>(a.n_rows) * a.heads + 3) / 4 > kThreads / 256) return false;
   *bytes = split ? grid * rows * (a.dim + 2) * 4 + a.n_requests * 8 : 0;
   return true;
 }

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(verify_slots_args a
     }
     if (mine) {
       a.slots[rows + lane] = slot(static_cast<int64_t>(c) + lane);
-      a.positions[rows + lane] = c + depth;
+      a.positions[rows + lane] = min(c, INT32_MAX - depth) + depth;
       a.masks[rows + lane] = static_cast<int64_t>(mask);
     }
   }
