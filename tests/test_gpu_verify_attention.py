@@ -128,6 +128,18 @@ def test_many_requests():
     Case(rng.integers(0, 900, 140), rows, 8, 1, 128, seed=2).check("most without rows")
 
 
+def test_very_many_requests():
+    rng = np.random.default_rng(7)
+    for B in (128, 129, 1024, 1025, 4200):
+        Case(rng.integers(0, 40, B), rng.integers(0, 4, B), 2, 2, 64, seed=B, pad=2).check(f"{B} requests")
+    rows = np.zeros(1100, int)
+    rows[[0, 7, 8, 500, 1099]] = [33, 64, 1, 20, 64]
+    Case(rng.integers(0, 90, 1100), rows, 16, 1, 64, seed=3).check("several row blocks, most without rows")
+    cached = np.zeros(1100, int)
+    cached[600] = 9000
+    Case(cached, np.ones(1100, int), 4, 2, 128, P=64, seed=4).check("one long context among many")
+
+
 def test_peaked_scores():
     for dtype in (BF, FH):
         Case([3000, 64], [4, 2], 4, 2, 128, dtype=dtype, qscale=30.0, seed=7).check("peaked")

@@ -184,6 +184,7 @@ def test_workspace_sizes(lib):
         return lib.verify_tree_attention_workspace(pack("attention", f))
     assert need(width=64) == 0            # 1024 tokens: one part
     assert need(width=65) > 0
+    assert need(width=64, n_requests=128) == 0 and need(width=64, n_requests=129) == 129 * 8   # the cut's plan
     assert need(n_rows=0) == 0 and need(scale=0.0) == INVALID
     f = base("logprobs")
     assert lib.verify_token_logprobs_workspace(pack("logprobs", f)) > 0

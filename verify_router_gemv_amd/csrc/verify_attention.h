@@ -23,8 +23,8 @@
 // 32 tokens' same piece hit different banks; values as they are.
 //
 // The context is split over blocks: the blocks that the chip holds at once are handed out by
-// rows * tokens of each request (worked out by every block from the lengths), and a second kernel joins
-// the parts of requests with more than one.
+// rows * tokens of each request (worked out from the lengths, by every block or, with many requests, by a
+// kernel of its own), and a last kernel joins the parts of requests with more than one.
 // Bound: memory (each K/V byte is read once) up to about 64 query rows a kv head; above, the
 // exponentials and the matrix cores.
 #pragma once
@@ -37,6 +37,7 @@ constexpr int kTile = 32;          // tokens per step of a wave
 // A context of more than kSplitTiles tiles per wave of a block is split, into parts of at least kMinTiles: a
 // tile more costs a wave about 2 us of latency, a split the second kernel, 5 us.
 constexpr int kSplitTiles = 4, kMinTiles = 2;
+constexpr int kScanRequests = 128;  // with more, a kernel of its own works the cut out (verify_attention_cut.h)
 constexpr int kCus = 256;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -50,9 +51,10 @@ struct AttnLaunch {
   int32_t grid;      // blocks launched
   int32_t least;     // fewest tiles of a part ...
   int32_t whole;     // ... and most of a context that is not split for the sake of the chip's width
+  int32_t split;     // 1: contexts may come in parts, joined by the second kernel
   int32_t swizzle;   // 1: several row blocks per request, kept on one XCD (8 neighbours)
   float* part;       // [grid][rows][D] partial outputs, then [grid][rows][2] (maximum, sum)
-  int32_t* plan;     // [B][2] first block and number of parts of each request, for the join
+  int32_t* plan;     // [B][2] first block and number of parts of each request
 };
 
 struct AttnRequest {
@@ -85,6 +87,42 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
   return v + (lane >= 16 ? t0 : 0) + (lane >= 32 ? t1 : 0) + (lane >= 48 ? t2 : 0);
 }
 
+// The last of n ascending numbers, `stride` apart, that is at most x (the first if none is): 64 of them a
+// step. Other than ascending numbers give some place of the n.
+__device__ __forceinline__ int wave_search(const int32_t* v, int stride, int n, int x, int lane) {
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64, at = lane * step;
+    const uint64_t hit = __ballot(at < n && v[static_cast<int64_t>(lo + (at < n ? at : 0)) * stride] <= x);
+    const int k = hit ? 63 - __clzll(static_cast<long long>(hit)) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// Tiles of a request, counted once per row block.
+__device__ __forceinline__ float attn_work(const AttnLaunch& p, const AttnRequest& q, int group) {
+  const int mbs = (q.rows * group + (1 << p.m_shift) - 1) >> p.m_shift;
+  return static_cast<float>(mbs) * static_cast<float>((q.len + kTile - 1) / kTile);
+}
+// Tiles per block so that the whole call makes about `target` blocks. (As float: rounding moves the cut,
+// alike in all blocks, and the grid has blocks to spare.)
+__device__ __forceinline__ unsigned attn_chunk(const verify_attention_args& a, const AttnLaunch& p, float work) {
+  const float c = ceilf(work * static_cast<float>(a.kv_heads) / static_cast<float>(p.target));
+  return max(static_cast<unsigned>(c), static_cast<unsigned>(p.least));
+}
+// The blocks of a request.
+__device__ __forceinline__ int attn_blocks(const verify_attention_args& a, const AttnLaunch& p, const AttnRequest& q,
+                                           int group, unsigned chunk, int* parts, int* mbs) {
+  const unsigned tiles = static_cast<unsigned>(q.len + kTile - 1) / kTile;
+  const bool split = tiles > max(chunk, static_cast<unsigned>(p.whole));
+  *parts = split ? static_cast<int>((tiles + chunk - 1) / chunk) : 1;
+  *mbs = (q.rows * group + (1 << p.m_shift) - 1) >> p.m_shift;
+  const int units = *parts * a.kv_heads;
+  return *mbs * (p.swizzle ? (units + 7) & ~7 : units);
+}
+
 // The request, row block, kv head and part of the context that block `at` works on; false: none. Called
 // by all lanes of a wave.
 struct AttnItem {
@@ -94,61 +132,63 @@ struct AttnItem {
 
 __device__ __forceinline__ bool attn_item(const verify_attention_args& a, const AttnLaunch& p, int lane, int group,
                                           int at, AttnItem* it) {
-  const int rnd = (1 << p.m_shift) - 1;
-  // Tiles per block so that the whole call makes about `target` blocks. (As float: rounding moves the
-  // cut, alike in all blocks, and the grid has blocks to spare.)
-  float work = 0;
-  AttnRequest q{0, 0, 0, 0};
-  for (int b = lane; b < a.n_requests; b += 64) {
-    q = attn_request(a, b);
-    work += static_cast<float>((q.rows * group + rnd) >> p.m_shift) * static_cast<float>((q.len + kTile - 1) / kTile);
-  }
-  work = wave_sum(work) * static_cast<float>(a.kv_heads);
-  const float c = ceilf(work / static_cast<float>(p.target));
-  const unsigned chunk = max(static_cast<unsigned>(c), static_cast<unsigned>(p.least));
-  int base = 0;
-  for (int b0 = 0; b0 < a.n_requests; b0 += 64) {
-    const int b = b0 + lane;
-    if (a.n_requests > 64) q = b < a.n_requests ? attn_request(a, b) : AttnRequest{0, 0, 0, 0};
-    const unsigned tiles = static_cast<unsigned>(q.len + kTile - 1) / kTile;
-    const bool split = tiles > max(chunk, static_cast<unsigned>(p.whole));
-    const int parts = split ? static_cast<int>((tiles + chunk - 1) / chunk) : 1;
-    const int mbs = (q.rows * group + rnd) >> p.m_shift;
-    int units = parts * a.kv_heads;
-    if (p.swizzle) units = (units + 7) & ~7;
-    const int blocks = mbs * units;
-    const int end = base + wave_scan(blocks, lane);
-    const uint64_t hit = __ballot(end > at);
-    if (hit) {
-      const int from = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      it->b = b0 + from;
-      it->q.start = __builtin_amdgcn_readlane(q.start, from);
-      it->q.rows = __builtin_amdgcn_readlane(q.rows, from);
-      it->q.cached = __builtin_amdgcn_readlane(q.cached, from);
-      it->q.len = __builtin_amdgcn_readlane(q.len, from);
-      it->parts = __builtin_amdgcn_readlane(parts, from);
-      const int n_mb = __builtin_amdgcn_readlane(mbs, from);
-      const int first = __builtin_amdgcn_readlane(end - blocks, from);
-      // A request's blocks in launch order: (part, head) units; with the swizzle in groups of 8, row blocks
-      // in between, so that the row blocks of one unit are 8 apart and reach the same XCD (and its L2).
-      int unit = at - first;
-      it->mb = 0;
-      if (p.swizzle) {
-        const int group8 = unit / (8 * n_mb), r = unit - group8 * 8 * n_mb;
-        it->mb = r >> 3;
-        unit = group8 * 8 + (r & 7);
-      }
-      if (p.plan && unit == 0 && it->mb == 0 && threadIdx.x == 0) {
-        p.plan[2 * it->b] = first;
-        p.plan[2 * it->b + 1] = it->parts;
-      }
-      it->part = unit / a.kv_heads;
-      it->head = unit - it->part * a.kv_heads;
-      return it->part < it->parts;  // the swizzle's rounding
+  const int B = a.n_requests;
+  int blocks = 0, first = 0, n_mb = 0;
+  if (B > kScanRequests) {
+    it->b = wave_search(p.plan, 2, B, at, lane);
+    it->q = attn_request(a, it->b);
+    first = p.plan[2 * it->b];
+    it->parts = p.plan[2 * it->b + 1];
+    n_mb = (it->q.rows * group + (1 << p.m_shift) - 1) >> p.m_shift;
+    if (n_mb == 0) return false;
+  } else {
+    float work = 0;
+    AttnRequest q{0, 0, 0, 0};
+    for (int b = lane; b < B; b += 64) {
+      q = attn_request(a, b);
+      work += attn_work(p, q, group);
     }
-    base = __builtin_amdgcn_readlane(end, 63);
+    const unsigned chunk = attn_chunk(a, p, wave_sum(work));
+    int base = 0, b0 = 0;
+    for (;; b0 += 64) {
+      if (b0 >= B) return false;
+      const int b = b0 + lane;
+      if (B > 64) q = b < B ? attn_request(a, b) : AttnRequest{0, 0, 0, 0};
+      int parts, mbs;
+      blocks = attn_blocks(a, p, q, group, chunk, &parts, &mbs);
+      const int end = base + wave_scan(blocks, lane);
+      const uint64_t hit = __ballot(end > at);
+      if (hit) {
+        const int from = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+        it->b = b0 + from;
+        it->q.start = __builtin_amdgcn_readlane(q.start, from);
+        it->q.rows = __builtin_amdgcn_readlane(q.rows, from);
+        it->q.cached = __builtin_amdgcn_readlane(q.cached, from);
+        it->q.len = __builtin_amdgcn_readlane(q.len, from);
+        it->parts = __builtin_amdgcn_readlane(parts, from);
+        n_mb = __builtin_amdgcn_readlane(mbs, from);
+        first = __builtin_amdgcn_readlane(end - blocks, from);
+        break;
+      }
+      base = __builtin_amdgcn_readlane(end, 63);
+    }
   }
-  return false;
+  // A request's blocks in launch order: (part, head) units; with the swizzle in groups of 8, row blocks
+  // in between, so that the row blocks of one unit are 8 apart and reach the same XCD (and its L2).
+  int unit = at - first;
+  it->mb = 0;
+  if (p.swizzle) {
+    const int group8 = unit / (8 * n_mb), r = unit - group8 * 8 * n_mb;
+    it->mb = r >> 3;
+    unit = group8 * 8 + (r & 7);
+  }
+  if (B <= kScanRequests && p.plan && unit == 0 && it->mb == 0 && threadIdx.x == 0) {
+    p.plan[2 * it->b] = first;
+    p.plan[2 * it->b + 1] = it->parts;
+  }
+  it->part = unit / a.kv_heads;
+  it->head = unit - it->part * a.kv_heads;
+  return it->part < it->parts;  // the swizzle's rounding
 }
 
 __device__ __forceinline__ int64_t attn_slot(const AttnLaunch& p, int first, int unit, int mb, int mbs) {
@@ -648,7 +688,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(verify_attention_args a,
   const int t = id / a.heads, hq = id - t * a.heads;
   if (t >= a.n_rows) return;
   int b = -1, start = 0, rows = 0;
-  for (int b0 = 0; b0 < a.n_requests && b < 0; b0 += 64) {
+  if (a.n_requests > kScanRequests) {
+    const int x = wave_search(a.row_start, 1, a.n_requests, t, lane);
+    const AttnRequest q = attn_request(a, x);
+    if (t >= q.start && t < q.start + q.rows) b = x, start = q.start, rows = q.rows;
+  }
+  for (int b0 = 0; b0 < (a.n_requests > kScanRequests ? 0 : a.n_requests) && b < 0; b0 += 64) {
     const int x = b0 + lane;
     AttnRequest q{0, 0, 0, 0};
     if (x < a.n_requests) q = attn_request(a, x);
@@ -750,17 +795,19 @@ inline bool attn_plan(const verify_attention_args& a, AttnLaunch* p, int64_t* by
   // A table that holds no more than that never splits.
   const bool split = static_cast<int64_t>(a.width) * a.page_size > p->whole * kTile;
   if (split && (static_cast<int64_t>(a.n_rows) * a.heads + 3) / 4 > kThreads / 256) return false;
-  *bytes = split ? grid * rows * (a.dim + 2) * 4 + a.n_requests * 8 : 0;
+  p->split = split;
+  *bytes = split ? grid * rows * (a.dim + 2) * 4 : 0;
+  if (split || a.n_requests > kScanRequests) *bytes += a.n_requests * 8;
   return true;
 }
 
 inline void attn_workspace(const verify_attention_args& a, AttnLaunch* p, void* workspace) {
   p->part = static_cast<float*>(workspace);
-  p->plan = reinterpret_cast<int32_t*>(p->part + (static_cast<int64_t>(p->grid) << p->m_shift) * (a.dim + 2));
+  p->plan = reinterpret_cast<int32_t*>(p->part + (p->split ? (static_cast<int64_t>(p->grid) << p->m_shift) * (a.dim + 2) : 0));
 }
 
 template <typename T, int D>
-hipError_t launch_attention_d(const verify_attention_args& a, const AttnLaunch& p, bool join, hipStream_t stream) {
+hipError_t launch_attention_d(const verify_attention_args& a, const AttnLaunch& p, hipStream_t stream) {
   constexpr int W = D == 256 ? 4 : 8;
   const dim3 grid(p.grid), block(64 * W);
   switch (attn_wm(a)) {
@@ -771,22 +818,22 @@ hipError_t launch_attention_d(const verify_attention_args& a, const AttnLaunch& 
       if constexpr (D != 256) attn_kernel<T, D, 8, 1><<<grid, block, 0, stream>>>(a, p);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !join) return e;
+  if (e != hipSuccess || !p.split) return e;
   const int64_t waves = static_cast<int64_t>(a.n_rows) * a.heads;
   attn_join_kernel<T, D><<<dim3(static_cast<unsigned>((waves + 3) / 4)), dim3(256), 0, stream>>>(a, p);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_attention(const verify_attention_args& a, const AttnLaunch& p, bool join, hipStream_t stream) {
+hipError_t launch_attention(const verify_attention_args& a, const AttnLaunch& p, hipStream_t stream) {
   switch (a.dim) {
-    case 64: return launch_attention_d<T, 64>(a, p, join, stream);
-    case 128: return launch_attention_d<T, 128>(a, p, join, stream);
-    default: return launch_attention_d<T, 256>(a, p, join, stream);
+    case 64: return launch_attention_d<T, 64>(a, p, stream);
+    case 128: return launch_attention_d<T, 128>(a, p, stream);
+    default: return launch_attention_d<T, 256>(a, p, stream);
   }
 }
 
-extern template hipError_t launch_attention<__bf16>(const verify_attention_args&, const AttnLaunch&, bool, hipStream_t);
-extern template hipError_t launch_attention<_Float16>(const verify_attention_args&, const AttnLaunch&, bool, hipStream_t);
+extern template hipError_t launch_attention<__bf16>(const verify_attention_args&, const AttnLaunch&, hipStream_t);
+extern template hipError_t launch_attention<_Float16>(const verify_attention_args&, const AttnLaunch&, hipStream_t);
 
 }  // namespace verify

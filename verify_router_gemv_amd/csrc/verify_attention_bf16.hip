@@ -1,5 +1,5 @@
 // Tree attention over bfloat16 caches.
 #include "verify_attention.h"
 namespace verify {
-template hipError_t launch_attention<__bf16>(const verify_attention_args&, const AttnLaunch&, bool, hipStream_t);
+template hipError_t launch_attention<__bf16>(const verify_attention_args&, const AttnLaunch&, hipStream_t);
 }  // namespace verify

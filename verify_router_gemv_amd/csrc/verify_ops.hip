@@ -1,5 +1,5 @@
 // The C entries of the verify-round operators: checks, launch shapes, launches.
-#include "verify_attention.h"
+#include "verify_attention_cut.h"
 #include "verify_internal.h"
 #include "verify_logprobs.h"
 #include "verify_rope.h"
@@ -51,8 +51,11 @@ extern "C" moe_status verify_tree_attention(const verify_attention_args* a, void
   if (!workspace_ok(workspace, workspace_bytes, bytes)) return MOE_ERR_INVALID_ARG;
   if (bytes) attn_workspace(*a, &p, workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return hip_status(a->type == VERIFY_BF16 ? launch_attention<__bf16>(*a, p, bytes != 0, s)
-                                           : launch_attention<_Float16>(*a, p, bytes != 0, s));
+  if (a->n_requests > kScanRequests) {
+    const hipError_t e = launch_attn_cut(*a, p, s);
+    if (e != hipSuccess) return hip_status(e);
+  }
+  return hip_status(a->type == VERIFY_BF16 ? launch_attention<__bf16>(*a, p, s) : launch_attention<_Float16>(*a, p, s));
 }
 
 extern "C" int64_t verify_token_logprobs_workspace(const verify_logprobs_args* a) {
