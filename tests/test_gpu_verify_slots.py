@@ -59,6 +59,7 @@ def test_trees(B, rows, context, P):
 
 @pytest.mark.parametrize("B,rows,context,P", [
     (1, 1, 0, 16), (1, 40000, 0, 16), (2, 3000, 65, 64), (3, 1, 131071, 256), (300, 200, 30, 16), (4096, 2, 9, 8),
+    (9001, 3, 40, 16),
 ])
 def test_chains(B, rows, context, P):
     rng = np.random.default_rng(B + rows)
