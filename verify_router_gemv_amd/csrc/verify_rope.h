@@ -7,7 +7,9 @@
 // way.  Angle and reduction to a turn are float64 (position * inv_freq * 1/(2 pi), 53 bits: a position of
 // 2^20 keeps its fraction of a turn to 2^-33), the sine and cosine of the remaining turn float32.  One
 // rounding at the end, to the cache's type.
-// Bound: memory from about a thousand rows, launch and two dependent load latencies below.
+// Bound: memory from about a thousand rows, launch and two dependent load latencies below.  Measured: 8191
+// rows of 16 + 2 heads of 256, fp16, 42 us (4.0 TB/s read and written); 64 rows of 32 + 8 heads of 128, fp32 in,
+// 4.2; one row of 16 + 2 heads 3.2.
 #pragma once
 
 #include "verify_common.h"
@@ -138,8 +140,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(verify_rope_args a) 
   }
 }
 
-// Rows alone fill the chip from 512 on; below, a row's heads are spread over blocks too (each block
-// computes the row's angles again).
+// Rows alone fill the chip from 512 on; below, a row's heads are spread over blocks too, each of which
+// computes the row's angles again (32 + 8 heads of 128, bf16, spread against one block a row: 64 rows 3.5, 4.4
+// us; 256 4.8, 5.4; 512 7.1, 6.7; 4096 40, 26).
 template <typename TI, typename TC, int D>
 hipError_t launch_rope_t(const verify_rope_args& a, hipStream_t stream) {
   constexpr int HB = kRopeThreads / (D / 8);
