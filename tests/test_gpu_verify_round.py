@@ -141,3 +141,24 @@ def test_a_captured_round_equals_the_eager_one():
                 assert torch.equal(a, b)
             hd += es.counts[1:]
             cached = cached + np.minimum(rows, 2).astype(np.int32)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_the_outputs_of_a_call_are_tensors_of_their_own(mode):
+    with mode():
+        x = normal(gen(3), 5, 999)
+        tokens = torch.randint(999, (5, 2), device=DEV)
+        lp = v.token_logprobs(x, tokens, top=4)
+        s = v.round_slots(i32([3, 20]), i32([2, 3]), i32(np.zeros((2, 4))), i32([7]), 16, 6, i32([-1, 0, -1, 0, 0, -1]))
+        for made in (lp, s):
+            before = [t.clone() for t in made]
+            for i, t in enumerate(made):
+                assert t.is_contiguous() and not t.requires_grad
+                t.add_(1)                        # changes none of the others
+                for j, (other, old) in enumerate(zip(made, before)):
+                    assert torch.equal(other, old + (j <= i)), f"{j} after a change of {i}"
+                assert torch.equal(t.flatten().view(-1), t.clone().flatten())
+        del lp, s, x                             # an output outlives its call's other tensors
+        lp = v.token_logprobs(normal(gen(4), 3, 50), None, top=1).top_logprobs
+        torch.cuda.synchronize()
+        assert lp.shape == (3, 1) and bool((lp < 0).all())

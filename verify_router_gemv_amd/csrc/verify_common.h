@@ -27,16 +27,6 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
   return v;
 }
 
-// Inclusive prefix sum over the wave.
-__device__ __forceinline__ int64_t wave_scan64(int64_t v, int lane) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const int64_t up = __shfl_up(v, s);
-    if (lane >= s) v += up;
-  }
-  return v;
-}
-
 // The word of lane ^ 16 (X = 16) or lane ^ 32 beside the lane's own, in either order.
 template <int X>
 __device__ __forceinline__ float2 across(float v) {
@@ -80,10 +70,6 @@ __device__ __forceinline__ int wave_max(int v) {
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return max(static_cast<int>(b[0]), static_cast<int>(b[1]));
 }
-__device__ __forceinline__ float lane_value(float v, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
-__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 __device__ __forceinline__ int max0(int v) { return v > 0 ? v : 0; }
 
