@@ -683,8 +683,8 @@ attn_kernel(verify_attention_args a, AttnLaunch p) {
 
 // Joins the parts of a (row, head), one wave each: lane i first takes part i's maximum and sum, then the
 // wave's halves take every other part's output, D / 32 values a lane: sixteen parts at once, or the last eight
-// (one row of 16 heads, 128 parts: 6.2 us, always eight 7.7; sixteen alone or 32 take registers that a call of
-// many rows misses). Rows of requests in one part are stored already.
+// (one row of 16 heads, 128 parts: 6.2 us, always eight 7.7; 32 at once 5.8, but 10.1 instead of 8.8 with 8192
+// rows of few parts, which miss the registers). Rows of requests in one part are stored already.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(verify_attention_args a, AttnLaunch p) {
   constexpr int E = D / 32;
